@@ -102,6 +102,34 @@ typedef struct {
   int64_t stride;
 } gns_batch;
 
+/* One tensor of a list (gns_grad_norm, gns_clip_grads, gns_adamw_step): a batch of rows with
+ * its element type (gns_dtype). Unlike a lone gns_batch it may start at any element, have any
+ * ld >= cols (ignored when rows == 1) and any stride that keeps the matrices apart (ignored
+ * when count == 1), hold up to 2^40 elements (a tensor without gaps; 2^31 - 1 rows and columns
+ * otherwise), and be empty (a dimension of 0; ptr may then be NULL). */
+typedef struct {
+  gns_batch x;
+  int32_t dtype;
+  int32_t reserved;
+} gns_tensor;
+
+/* Norm of a list of gradients. */
+typedef enum {
+  GNS_NORM_L2 = 0, /* square root of the sum of squares of all elements */
+  GNS_NORM_INF = 1 /* largest magnitude */
+} gns_norm_type;
+
+/* AdamW hyper-parameters. step is t >= 1, the number of this step (the first is 1). */
+typedef struct {
+  double lr;
+  double beta1;
+  double beta2;
+  double eps;
+  double weight_decay;
+  int32_t step;
+  int32_t reserved;
+} gns_adamw_params;
+
 /* Newton-Schulz schedule: T iterations with coefficients (a_t, b_t, c_t), t = 1..T
  * (index t-1), e.g. a caller's Polar Express table. Bit i of restart_mask (1 <= i < T)
  * restarts after iteration i (Dion3 Algorithm 3 restarts after iteration 2: mask 1u << 2).
@@ -249,6 +277,49 @@ GNS_API int gns_muon_step(const gns_batch* W, const gns_batch* G, const gns_batc
  * selected rows of the oriented matrix). */
 GNS_API int gns_frac_row_select(const gns_batch* m, int k, int32_t* idx, const gns_batch* gathered, void* ws,
                         size_t ws_bytes, void* stream);
+
+/* ---- a training step around Muon: lists of tensors of any shapes and types ----
+ *
+ * A list is an array of n gns_tensor, n >= 1; bf16, fp16 and fp32 tensors may be mixed in it.
+ * Tensors of one list may not overlap one another. A call makes one launch for about a
+ * thousand (AdamW: five hundred) tensors, more launches for longer lists. */
+
+/* Bytes of workspace of gns_grad_norm and gns_clip_grads for a list of n tensors (0 and the
+ * last error when n < 1). */
+GNS_API size_t gns_list_workspace_size(int n);
+
+/* Global norm of the gradients, and the scale that clips them:
+ *   result[0] = N = sqrt(sum over all tensors and elements of g^2), or max |g| (norm_type)
+ *   result[1] = min(1, max_norm / (N + eps)); 1 when max_norm is infinity (no clipping)
+ * result: two device floats. Sums are formed in a fixed order (the same bits for the same
+ * list and sizes), squares never overflow or vanish: N is right over the whole range of the
+ * types. A NaN gradient gives N = NaN and a NaN scale, an infinite one N = inf and scale 0;
+ * either sets GNS_DEVST_NONFINITE. A list of empty tensors has N = 0. max_norm >= 0 and not
+ * NaN, eps >= 0 and finite. */
+GNS_API int gns_grad_norm(const gns_tensor* grads, int n, int norm_type, float max_norm, float eps, float* result,
+                          void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* gns_grad_norm, and every gradient multiplied by result[1] in fp32 and rounded once to its
+ * type: in place when outs is NULL, else into outs[i] (same shape and dtype as grads[i]; the
+ * same buffers with the same layout, or buffers that overlap no gradient). */
+GNS_API int gns_clip_grads(const gns_tensor* grads, const gns_tensor* outs, int n, int norm_type, float max_norm,
+                           float eps, float* result, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* One AdamW step of n tensors (the parameters beside Muon's matrices), in fp32 arithmetic:
+ *   g <- c G;  M <- beta1 M + (1 - beta1) g;  V <- beta2 V + (1 - beta2) g^2
+ *   W <- (1 - lr weight_decay) W - lr / (1 - beta1^t) M / (sqrt(V / (1 - beta2^t)) + eps)
+ * W and G: bf16, fp16 or fp32, each of its own type; M, V: fp32. c = *grad_scale (device, e.g.
+ * result + 1 of gns_grad_norm: clipping then costs no pass over the gradients), 1 when NULL.
+ * master (nullable; also tensor by tensor, by an empty gns_tensor): the fp32 copy of a 16-bit
+ * weight, which is updated in W's place, W receiving it rounded once; without one W itself is
+ * read, updated and rounded once. step_count (nullable, device): t is read from there (values
+ * below 1 count as 1) instead of adamw->step, so that a captured step can be replayed. All
+ * roles of a tensor have the same shape; each may have its own ld and stride; they may not
+ * alias. A weight that becomes non-finite sets GNS_DEVST_NONFINITE. beta1, beta2 in [0, 1),
+ * eps > 0. */
+GNS_API int gns_adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, const gns_tensor* V,
+                           const gns_tensor* master, int n, const gns_adamw_params* adamw, const float* grad_scale,
+                           const int32_t* step_count, int32_t* dev_status, void* stream);
 
 /* Self-test of the failure detection every kernel of the library relies on (no GPU fault is
  * involved). Launches one thread that waits, through the same bounded-wait code the GEMM

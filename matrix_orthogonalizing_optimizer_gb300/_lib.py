@@ -25,6 +25,8 @@ GNS_OP_GRAM_NS = 0
 GNS_OP_NS_STANDARD = 1
 GNS_OP_MUON_STEP = 2
 GNS_OP_FRAC_SELECT = 3
+GNS_NORM_L2 = 0
+GNS_NORM_INF = 1
 GNS_MAX_T = 16
 GNS_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -34,12 +36,23 @@ EXPORTS = [
     "gns_gram_ns_batched", "gns_ns_standard_batched", "gns_sym_gemm_xxt", "gns_sym_gemm",
     "gns_sym_poly_update", "gns_muon_step", "gns_frac_row_select", "gns_profile_set", "gns_profile_query", "gns_gram_ns_batched_noalloc",
     "gns_selftest_bounded_wait",
+    "gns_list_workspace_size", "gns_grad_norm", "gns_clip_grads", "gns_adamw_step",
 ]
 
 
 class GnsBatch(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("count", ctypes.c_int64), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("stride", ctypes.c_int64)]
+
+
+class GnsTensor(ctypes.Structure):
+    _fields_ = [("x", GnsBatch), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class GnsAdamwParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class GnsNsParams(ctypes.Structure):
@@ -110,6 +123,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gns_frac_row_select.argtypes = [B, i32, vp, B, vp, sz, vp]
     lib.gns_gram_ns_batched_noalloc.restype = i32
     lib.gns_gram_ns_batched_noalloc.argtypes = [B, B, i32, i32, P(GnsNsParams), vp, vp]
+    # lists of tensors: arrays of GnsTensor passed by address (a TensorList keeps its own)
+    lib.gns_list_workspace_size.restype = sz
+    lib.gns_list_workspace_size.argtypes = [i32]
+    lib.gns_grad_norm.restype = i32
+    lib.gns_grad_norm.argtypes = [vp, i32, i32, f32, f32, vp, vp, sz, vp, vp]
+    lib.gns_clip_grads.restype = i32
+    lib.gns_clip_grads.argtypes = [vp, vp, i32, i32, f32, f32, vp, vp, sz, vp, vp]
+    lib.gns_adamw_step.restype = i32
+    lib.gns_adamw_step.argtypes = [vp, vp, vp, vp, vp, i32, P(GnsAdamwParams), vp, vp, vp, vp]
     lib.gns_selftest_bounded_wait.restype = i32
     lib.gns_selftest_bounded_wait.argtypes = [vp, i32, ctypes.c_uint32, vp, vp, vp]
     lib.gns_profile_set.restype = i32

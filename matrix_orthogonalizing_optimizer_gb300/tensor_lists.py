@@ -1,0 +1,248 @@
+"""Python API of the operators over lists of tensors: the global gradient norm, clipping by it,
+and the AdamW step of the parameters beside Muon's matrices (embeddings, heads, gains, biases).
+
+A list may mix shapes and dtypes (bfloat16, float16, float32). Its tensors are CUDA tensors
+without gaps in memory (contiguous, or a permutation of a contiguous tensor such as a
+transpose), or batches of rows with a pitch: leading dimensions that collapse to one, then
+rows, then a contiguous last dimension. They may start at any element. Every call takes a
+plain sequence of tensors or a TensorList, which describes the tensors to the library once; a
+program that keeps its parameters, states and gradients in the same buffers keeps their
+TensorLists too.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from dataclasses import dataclass
+from typing import Optional, Sequence, Union
+
+import torch
+
+from . import _lib
+from ._lib import GnsAdamwParams, GnsTensor, load
+from ._lib import check as check_rc
+from .api import _CallStatus, _dtype_code, _stream_ptr, alloc_workspace
+
+
+def _describe(e: GnsTensor, t: torch.Tensor):
+    """Fills the descriptor of one tensor; returns what has to agree between the roles of an
+    operator: its shape, and the order of its dimensions in memory unless that is the usual."""
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    e.dtype = _dtype_code(t)
+    e.x.ptr = t.data_ptr()
+    shape = tuple(t.shape)
+    if t.is_contiguous():
+        if len(shape) <= 1:
+            count, rows, cols = 1, 1, t.numel()
+        elif len(shape) == 2:
+            count, (rows, cols) = 1, shape
+        else:
+            count, rows, cols = math.prod(shape[:-2]), shape[-2], shape[-1]
+        e.x.count, e.x.rows, e.x.cols, e.x.ld, e.x.stride = count, rows, cols, cols, rows * cols
+        return shape
+    order = tuple(sorted(range(len(shape)), key=lambda d: (-t.stride(d), -shape[d], d)))
+    u = t.permute(order)
+    if u.is_contiguous():
+        _describe(e, u)
+        return shape, order
+    # leading dimensions that lie evenly behind one another are one
+    dims, steps = list(shape), list(t.stride())
+    while len(dims) > 3 and (dims[0] == 1 or steps[0] == steps[1] * dims[1]):
+        d0 = dims.pop(0)
+        steps.pop(0)
+        dims[0] *= d0
+    while len(dims) < 3:
+        dims.insert(0, 1)
+        steps.insert(0, 0)
+    (count, rows, cols), (stride, ld, one) = dims[-3:], steps[-3:]
+    if len(dims) > 3 or (one != 1 and cols > 1) or (rows > 1 and ld < cols) or (
+            count > 1 and stride < (rows - 1) * ld * (rows > 1) + cols):
+        raise ValueError(f"a tensor of shape {shape} with strides {tuple(t.stride())} is neither without gaps nor a "
+                         "batch of rows with a contiguous last dimension: make it contiguous")
+    e.x.count, e.x.rows, e.x.cols, e.x.ld, e.x.stride = count, rows, cols, max(ld, cols), stride
+    return shape
+
+
+class TensorList:
+    """The library's descriptors of a list of tensors, which it keeps alive. Made once for
+    buffers that stay where they are; a tensor that got new memory needs a new TensorList. An
+    entry may be None (an AdamW master that a tensor has not)."""
+
+    def __init__(self, tensors: Sequence[Optional[torch.Tensor]]):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("need at least one tensor")
+        self.array = (GnsTensor * len(self.tensors))()
+        self.address = ctypes.addressof(self.array)
+        self.device = None
+        layout = []
+        for e, t in zip(self.array, self.tensors):
+            if t is None:
+                layout.append(None)
+                continue
+            layout.append(_describe(e, t))
+            if self.device is None:
+                self.device = t.device
+            elif self.device != t.device:
+                raise ValueError("the tensors of a list must live on one device")
+        self.has_none = None in layout
+        # compared as text: two lists of hundreds of tensors in a fraction of a microsecond
+        self.layout = layout
+        self.layout_text = repr(layout)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def tensor_list(tensors: Union[TensorList, torch.Tensor, Sequence[Optional[torch.Tensor]]]) -> TensorList:
+    """The TensorList of a sequence of tensors (or of one tensor); a TensorList is itself."""
+    if isinstance(tensors, TensorList):
+        return tensors
+    return TensorList([tensors] if isinstance(tensors, torch.Tensor) else tensors)
+
+
+def _same_layout(name: str, a: TensorList, b: TensorList, optional: bool = False) -> None:
+    if a.layout_text == b.layout_text:
+        return
+    if len(a) != len(b):
+        raise ValueError(f"{name}: {len(b)} tensors, expected {len(a)}")
+    for i, (x, y) in enumerate(zip(a.layout, b.layout)):
+        if x != y and not (optional and y is None):
+            raise ValueError(f"{name}[{i}]: shape (and order in memory) {y}, expected {x}")
+
+
+def list_workspace_size(n: int) -> int:
+    """Bytes of workspace grad_norm and clip_grads need for a list of n tensors."""
+    need = load().gns_list_workspace_size(int(n))
+    if need == 0:
+        raise _lib.GnsError(f"list_workspace_size: {_lib.last_error()}")
+    return int(need)
+
+
+_NORMS = {2: _lib.GNS_NORM_L2, math.inf: _lib.GNS_NORM_INF}
+
+
+def _norm_code(norm_type) -> int:
+    code = _NORMS.get(norm_type)
+    if code is None:
+        raise ValueError("norm_type must be 2 or math.inf")
+    return code
+
+
+def _norm_buffers(grads: TensorList, result, workspace, stream):
+    if grads.has_none:
+        raise ValueError("every gradient must be a tensor")
+    if result is None:
+        result = torch.empty(2, dtype=torch.float32, device=grads.device)
+        if stream is not None:
+            result.record_stream(stream)
+    elif result.dtype != torch.float32 or not result.is_cuda or result.numel() != 2 or not result.is_contiguous():
+        raise ValueError("result must be a contiguous CUDA float32 tensor of 2 entries")
+    if workspace is None:
+        workspace = alloc_workspace(list_workspace_size(len(grads)), grads.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    return result, workspace
+
+
+def grad_norm(grads, max_norm: Optional[float] = None, norm_type: float = 2.0, eps: float = 1e-6, result=None,
+              workspace=None, status=None, stream=None, check: bool = True) -> torch.Tensor:
+    """Global norm of a list of gradients: the square root of the sum of squares over all of
+    them (norm_type 2), or their largest magnitude (math.inf). Returns `result`, a float32
+    tensor: result[0] the norm, result[1] the scale min(1, max_norm / (norm + eps)) that clips
+    the gradients to max_norm (1 without max_norm), which adamw_step and muon_step take as
+    grad_scale without a pass over the gradients. A norm that is not finite is a device
+    condition (see gram_ns_batched): it raises GnsDeviceError unless `status` is given or
+    `check` is off."""
+    g = tensor_list(grads)
+    code = _norm_code(norm_type)
+    result, ws = _norm_buffers(g, result, workspace, stream)
+    cs = _CallStatus(status, g.device, check, stream)
+    rc = load().gns_grad_norm(g.address, len(g), code, math.inf if max_norm is None else float(max_norm), float(eps),
+                              result.data_ptr(), ws.data_ptr(), ws.numel(), cs.ptr(), _stream_ptr(stream, g.device))
+    check_rc(rc, "gns_grad_norm")
+    cs.done("gns_grad_norm")
+    return result
+
+
+def clip_grads(grads, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, outs=None, result=None,
+               workspace=None, status=None, stream=None, check: bool = True) -> torch.Tensor:
+    """Clips a list of gradients to the global norm max_norm: each is multiplied by grad_norm's
+    scale, in place or, with `outs` (a list of the same shapes and dtypes), into other buffers.
+    Returns `result` as grad_norm does (the norm before clipping, the scale)."""
+    g = tensor_list(grads)
+    code = _norm_code(norm_type)
+    out_address = None
+    if outs is not None:
+        o = tensor_list(outs)
+        _same_layout("outs", g, o)
+        out_address = o.address
+    result, ws = _norm_buffers(g, result, workspace, stream)
+    cs = _CallStatus(status, g.device, check, stream)
+    rc = load().gns_clip_grads(g.address, out_address, len(g), code, float(max_norm), float(eps), result.data_ptr(),
+                               ws.data_ptr(), ws.numel(), cs.ptr(), _stream_ptr(stream, g.device))
+    check_rc(rc, "gns_clip_grads")
+    cs.done("gns_clip_grads")
+    return result
+
+
+@dataclass
+class AdamWParams:
+    """Hyper-parameters of one AdamW step (gns_adamw_params); step is the number of the step, 1
+    for the first."""
+    lr: float
+    beta1: float = 0.9
+    beta2: float = 0.999
+    eps: float = 1e-8
+    weight_decay: float = 0.01
+    step: int = 1
+
+    def c_struct(self) -> GnsAdamwParams:
+        return GnsAdamwParams(float(self.lr), float(self.beta1), float(self.beta2), float(self.eps),
+                              float(self.weight_decay), int(self.step))
+
+
+def _device_scalar(name: str, t: Optional[torch.Tensor], dtype) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_cuda or t.numel() != 1:
+        raise ValueError(f"{name} must be a CUDA tensor of one {str(dtype)[6:]}")
+    return t.data_ptr()
+
+
+def adamw_step(W, G, M, V, lr: Optional[float] = None, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.01, step: int = 1, masters=None, params: Optional[AdamWParams] = None,
+               grad_scale: Optional[torch.Tensor] = None, step_count: Optional[torch.Tensor] = None, status=None,
+               stream=None, check: bool = True):
+    """One AdamW step in place on the lists W (weights), M and V (float32 first and second
+    moments) with the gradients G; `params` supplies every hyper-parameter when given.
+
+    masters: float32 copies of 16-bit weights (None for a weight that has none): the master is
+        updated and W receives it rounded.
+    grad_scale: a CUDA float32 tensor of one element that multiplies the gradients, e.g.
+        result[1:] of grad_norm.
+    step_count: a CUDA int32 tensor of one element that holds the step's number in place of
+        `step`; a step captured into a CUDA graph needs it, as the graph replays `step` as it was."""
+    w, g, m, v = tensor_list(W), tensor_list(G), tensor_list(M), tensor_list(V)
+    if params is None:
+        if lr is None:
+            raise ValueError("adamw_step needs lr (or params)")
+        params = AdamWParams(lr, beta1, beta2, eps, weight_decay, step)
+    if w.has_none:
+        raise ValueError("every weight must be a tensor")
+    _same_layout("G", w, g)
+    _same_layout("M", w, m)
+    _same_layout("V", w, v)
+    master_address = None
+    if masters is not None:
+        p = tensor_list(masters)
+        _same_layout("masters", w, p, optional=True)
+        master_address = p.address
+    cs = _CallStatus(status, w.device, check, stream)
+    rc = load().gns_adamw_step(w.address, g.address, m.address, v.address, master_address, len(w),
+                               ctypes.byref(params.c_struct()), _device_scalar("grad_scale", grad_scale, torch.float32),
+                               _device_scalar("step_count", step_count, torch.int32), cs.ptr(),
+                               _stream_ptr(stream, w.device))
+    check_rc(rc, "gns_adamw_step")
+    cs.done("gns_adamw_step")
