@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
+#include <type_traits>
 
 #include "../../include/gns.h"
 #include "common.cuh"
@@ -28,7 +29,13 @@ int set_error(int code, const std::string& msg);  // sets gns_last_error(); defi
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int MAX_GRID = 1216;  // blocks of one norm launch, and its partial sums (8 for each of 152 SMs)
+constexpr int MAX_GRID = 1216;  // blocks of one norm launch, and its partial sums
+#ifndef NORM_BLOCKS
+#define NORM_BLOCKS 8
+#endif
+#ifndef CLIP_BLOCKS
+#define CLIP_BLOCKS 4
+#endif
 
 // ---------------------------------------------------------------------------------------
 // lists as kernel parameters (at most 32,764 bytes of parameters a launch)
@@ -202,32 +209,33 @@ GNS_DEV int find_tensor(const L& l, int chunk) {
   return lo;
 }
 
-// Where unit j of a chunk of tensor t lies in every role; returns how many of its 8 elements
-// exist (0: none).
-template <int UNITS, int R, int CAP>
-GNS_DEV int locate(const FlatList<R, CAP>& l, int t, int chunk, int j, long long (&off)[R]) {
-  const long long o = l.head[t] + (static_cast<long long>(chunk - l.start[t]) * (THREADS * UNITS) + j) * 8;
+// Where unit j of a chunk of tensor t lies in every role, for units of 2^LOG elements and `per`
+// units a chunk; returns how many of its elements exist (0: none).
+template <int R, int CAP>
+GNS_DEV int locate(const FlatList<R, CAP>& l, int t, int chunk, int per, int log, int j, long long (&off)[R]) {
+  const long long o = l.head[t] + ((static_cast<long long>(chunk - l.start[t]) * per + j) << log);
 #pragma unroll
   for (int r = 0; r < R; ++r) off[r] = o;
-  const long long left = l.n[t] - o;
-  return left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
+  const long long left = l.n[t] - o, most = 1 << log;
+  return static_cast<int>(max(0ll, min(left, most)));
 }
 
-template <int UNITS, int R, int CAP>
-GNS_DEV int locate(const RowList<R, CAP>& l, int t, int chunk, int j, long long (&off)[R]) {
-  const uint32_t per_row = (static_cast<uint32_t>(l.cols[t]) + 7u) >> 3;
-  const long long u0 = static_cast<long long>(chunk - l.start[t]) * (THREADS * UNITS);
+template <int R, int CAP>
+GNS_DEV int locate(const RowList<R, CAP>& l, int t, int chunk, int per, int log, int j, long long (&off)[R]) {
+  const uint32_t cols = static_cast<uint32_t>(l.cols[t]), width = 1u << log;
+  const uint32_t per_row = (cols + width - 1u) >> log;
+  const long long u0 = static_cast<long long>(chunk - l.start[t]) * per;
   const long long row0 = u0 / per_row;
   const uint32_t x = static_cast<uint32_t>(u0 - row0 * per_row) + static_cast<uint32_t>(j);
   const uint32_t q = x / per_row;
   const long long row = row0 + q;
   if (row >= l.nrows[t]) return 0;
-  const uint32_t c = (x - q * per_row) * 8u;
+  const uint32_t c = (x - q * per_row) << log;
   const uint32_t b = static_cast<uint32_t>(row) / static_cast<uint32_t>(l.rows[t]);
   const uint32_t i = static_cast<uint32_t>(row) - b * static_cast<uint32_t>(l.rows[t]);
 #pragma unroll
   for (int r = 0; r < R; ++r) off[r] = b * l.stride[r][t] + i * l.ld[r][t] + c;
-  return static_cast<int>(min(8u, static_cast<uint32_t>(l.cols[t]) - c));
+  return static_cast<int>(min(width, cols - c));
 }
 
 // Elements before the first unit of a flat tensor: one for each of the first threads of its
@@ -270,84 +278,166 @@ GNS_DEV uint32_t block_max(uint32_t v) {
 }
 
 // ---------------------------------------------------------------------------------------
+// vectors: 16 bytes of one role, 8 values of a 16-bit type or 4 of f32
+
+struct Vec {
+  uint32_t w[4];
+};
+
+GNS_DEV int vec_log(int dt) { return dt == GNS_F32 ? 2 : 3; }
+
+// `valid` elements from `off` on; the others read as zero. align != 0: a whole vector starts on
+// 16 bytes.
+GNS_DEV void load_vec(Vec& u, const void* base, long long off, int log, int align, int valid) {
+  if (valid == (1 << log) && align) {
+    ld_v4(u.w, static_cast<const char*>(base) + (off << (4 - log)));
+  } else if (log == 2) {
+    const uint32_t* p = static_cast<const uint32_t*>(base) + off;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u.w[e] = e < valid ? p[e] : 0u;
+  } else {
+    const unsigned short* p = static_cast<const unsigned short*>(base) + off;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t lo = 2 * e < valid ? p[2 * e] : 0u, hi = 2 * e + 1 < valid ? p[2 * e + 1] : 0u;
+      u.w[e] = lo | (hi << 16);
+    }
+  }
+}
+
+GNS_DEV void store_vec(const Vec& u, void* base, long long off, int log, int align, int valid) {
+  if (valid == (1 << log) && align) {
+    st_v4(static_cast<char*>(base) + (off << (4 - log)), u.w);
+  } else if (log == 2) {
+    uint32_t* p = static_cast<uint32_t*>(base) + off;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < valid) p[e] = u.w[e];
+  } else {
+    unsigned short* p = static_cast<unsigned short*>(base) + off;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < valid) p[e] = static_cast<unsigned short>(u.w[e / 2] >> (16 * (e & 1)));
+  }
+}
+
+// The two values of a word of a 16-bit type.
+template <int DT>
+GNS_DEV float2 halves(uint32_t w) {
+  if (DT == GNS_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// ---------------------------------------------------------------------------------------
 // norm: sqrt(sum x^2) over the whole list, or max |x|
 
-constexpr int NORM_UNITS = 4;
+constexpr int NORM_VEC = 4;
 
-// Calls f(unit, type) for every unit of this block's chunks.
-template <int UNITS, class L, class F>
-GNS_DEV void for_units(const L& l, F f) {
+// Calls f(vectors, type) for this block's chunks, NORM_VEC vectors a thread at a time.
+template <class L, class F>
+GNS_DEV void for_vectors(const L& l, F f) {
   const int total = l.start[l.count];
   int chunk = blockIdx.x;
   if (chunk >= total) return;
   int t = find_tensor(l, chunk);
   for (; chunk < total; chunk += gridDim.x) {
     while (l.start[t + 1] <= chunk) ++t;
-    const int dt = l.type[t] & 3, align = l.align[t];
+    const int dt = l.type[t] & 3, log = vec_log(dt), align = l.align[t];
     const void* p = l.ptr[0][t];
-    Unit u[UNITS];
+    Vec u[NORM_VEC];
 #pragma unroll
-    for (int k = 0; k < UNITS; ++k) {
+    for (int k = 0; k < NORM_VEC; ++k) {
       long long off[1];
-      const int valid = locate<UNITS>(l, t, chunk, k * THREADS + static_cast<int>(threadIdx.x), off);
-      load_unit(u[k], p, off[0], dt == GNS_F32, align, valid);
+      const int valid = locate(l, t, chunk, THREADS * NORM_VEC, log, k * THREADS + static_cast<int>(threadIdx.x), off);
+      load_vec(u[k], p, off[0], log, align, valid);
     }
-#pragma unroll
-    for (int k = 0; k < UNITS; ++k) f(u[k], dt);
     if (static_cast<int>(threadIdx.x) < head_here(l, t, chunk)) {
-      load_unit(u[0], p, threadIdx.x, dt == GNS_F32, 0, 1);
-      f(u[0], dt);
+      Vec h[NORM_VEC] = {};
+      load_vec(h[0], p, threadIdx.x, log, 0, 1);
+      f(h, dt);
     }
+    f(u, dt);
   }
 }
 
-// Sum of (pre x)^2 over this block's chunks: 8 squares at a time in f32, these sums in f64.
-template <class L>
+// f32 sum of the squares of a thread's vectors of one chunk, the values scaled by `pre` first
+// (SCALED).
+template <int DT, bool SCALED>
+GNS_DEV float squares(const Vec (&u)[NORM_VEC], float pre) {
+  float q[2] = {0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < NORM_VEC; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (DT == GNS_F32) {
+        const float x = __uint_as_float(u[k].w[e]) * (SCALED ? pre : 1.f);
+        q[e & 1] = fmaf(x, x, q[e & 1]);
+      } else {
+        float2 x = halves<DT>(u[k].w[e]);
+        if (SCALED) x = make_float2(x.x * pre, x.y * pre);
+        q[0] = fmaf(x.x, x.x, q[0]);
+        q[1] = fmaf(x.y, x.y, q[1]);
+      }
+    }
+  return q[0] + q[1];
+}
+
+// Sum of squares over this block's chunks: a thread's up to 32 squares of a chunk in f32, these
+// sums in f64 (one conversion and one sum a chunk: at one for each 8 squares the f64 pipe bounds
+// the kernel).
+template <bool SCALED, class L>
 GNS_DEV double sum_squares(const L& l, float pre, uint32_t* bits) {
   double s = 0.0;
-  for_units<NORM_UNITS>(l, [&](const Unit& u, int dt) {
-    float x[8];
-    unpack(x, u, dt);
-    float q = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = x[e] * pre;
-      q = fmaf(v, v, q);
-      *bits |= __float_as_uint(x[e]);
-    }
+  for_vectors(l, [&](const Vec (&u)[NORM_VEC], int dt) {
+    const float q = dt == GNS_F32    ? squares<GNS_F32, SCALED>(u, pre)
+                    : dt == GNS_BF16 ? squares<GNS_BF16, SCALED>(u, pre)
+                                     : squares<GNS_F16, SCALED>(u, pre);
     s += static_cast<double>(q);
+    if (!SCALED) {
+#pragma unroll
+      for (int k = 0; k < NORM_VEC; ++k) *bits |= (u[k].w[0] | u[k].w[1]) | (u[k].w[2] | u[k].w[3]);
+    }
   });
   return s;
 }
 
-// part[blockIdx.x] = the block's sum of squares (inf = 0) or largest magnitude (inf = 1).
+// part[blockIdx.x] = the block's sum of squares (INF = false) or largest magnitude (INF = true).
 //
 // Squares of f32 and bf16 values leave f32's range long before the values do (above 2^64, below
 // 2^-63). A block whose sum says that this has happened (it is not finite, or below 2^-80 though
-// some value is not zero) sums once more with the values scaled by 2^-100 or 2^100, which is
-// exact for every value that counts: the largest magnitudes become at most 2^28, and where the
-// sum lies below 2^-80 none is above 2^-40, so they become at most 2^60. f64 holds the result.
-template <class L>
-__global__ void __launch_bounds__(THREADS) norm_part_kernel(const __grid_constant__ L l, int inf, double* part) {
-  if (inf) {
+// some bit is set) sums once more with the values scaled by 2^-100 or 2^100, which is exact for
+// every value that counts: the largest magnitudes become at most 2^28, and where the sum lies
+// below 2^-80 none is above 2^-40, so they become at most 2^60. f64 holds the result.
+template <bool INF, class L>
+__global__ void __launch_bounds__(THREADS, NORM_BLOCKS) norm_part_kernel(const __grid_constant__ L l, double* part) {
+  grid_dep_launch();
+  if (INF) {
     uint32_t m = 0;  // magnitudes order as their bits do, with every NaN above infinity
-    for_units<NORM_UNITS>(l, [&](const Unit& u, int dt) {
-      float x[8];
-      unpack(x, u, dt);
+    for_vectors(l, [&](const Vec (&u)[NORM_VEC], int dt) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+      for (int k = 0; k < NORM_VEC; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = u[k].w[e];
+          if (dt == GNS_F32) {
+            m = max(m, w & 0x7fffffffu);
+          } else {
+            const float2 x = dt == GNS_BF16 ? halves<GNS_BF16>(w) : halves<GNS_F16>(w);
+            m = max(m, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
+          }
+        }
     });
     m = block_max(m);
     if (threadIdx.x == 0) part[blockIdx.x] = static_cast<double>(__uint_as_float(m));
     return;
   }
   uint32_t bits = 0;
-  double s = block_sum(sum_squares(l, 1.f, &bits));
-  const int any = __syncthreads_or((bits & 0x7fffffffu) != 0);
+  double s = block_sum(sum_squares<false>(l, 1.f, &bits));
+  const int any = __syncthreads_or(bits != 0);
   if (!(s <= 1e38))
-    s = block_sum(sum_squares(l, 0x1p-100f, &bits)) * 0x1p200;
+    s = block_sum(sum_squares<true>(l, 0x1p-100f, &bits)) * 0x1p200;
   else if (s < 0x1p-80 && any)
-    s = block_sum(sum_squares(l, 0x1p100f, &bits)) * 0x1p-200;
+    s = block_sum(sum_squares<true>(l, 0x1p100f, &bits)) * 0x1p-200;
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
@@ -360,7 +450,9 @@ struct Finish {
   float eps;
 };
 
+// The norm and the scale, in every thread of the block.
 GNS_DEV void finish_norm(const Finish& f, float* norm, float* scale) {
+  __shared__ float out[2];
   double n = 0.0;
   if (f.inf) {
     uint32_t m = 0;
@@ -368,16 +460,20 @@ GNS_DEV void finish_norm(const Finish& f, float* norm, float* scale) {
     n = static_cast<double>(__uint_as_float(block_max(m)));
   } else {
     for (int i = threadIdx.x; i < f.nparts; i += THREADS) n += f.part[i];
-    n = sqrt(block_sum(n));
+    n = block_sum(n);
   }
-  *norm = static_cast<float>(n);
-  const double c = static_cast<double>(f.max_norm) / (n + static_cast<double>(f.eps));
-  *scale = isinf(f.max_norm) || c >= 1.0 ? 1.f : static_cast<float>(c);  // a NaN norm gives a NaN scale
+  if (threadIdx.x == 0) {
+    if (!f.inf) n = sqrt(n);
+    out[0] = static_cast<float>(n);
+    const double c = static_cast<double>(f.max_norm) / (n + static_cast<double>(f.eps));
+    out[1] = isinf(f.max_norm) || c >= 1.0 ? 1.f : static_cast<float>(c);  // a NaN norm gives a NaN scale
+  }
+  __syncthreads();
+  *norm = out[0];
+  *scale = out[1];
 }
 
-__global__ void __launch_bounds__(THREADS) norm_finish_kernel(Finish f, float* result, int* status) {
-  float norm, scale;
-  finish_norm(f, &norm, &scale);
+GNS_DEV void write_result(float norm, float scale, float* result, int* status) {
   if (threadIdx.x == 0) {
     result[0] = norm;
     result[1] = scale;
@@ -385,46 +481,80 @@ __global__ void __launch_bounds__(THREADS) norm_finish_kernel(Finish f, float* r
   }
 }
 
+__global__ void __launch_bounds__(THREADS) norm_finish_kernel(Finish f, float* result, int* status) {
+  grid_dep_wait();
+  float norm, scale;
+  finish_norm(f, &norm, &scale);
+  write_result(norm, scale, result, status);
+}
+
 // ---------------------------------------------------------------------------------------
 // clipping: out = round(scale * g); roles: gradient, output (the same pointers in place)
 
-constexpr int CLIP_UNITS = 2;
+constexpr int CLIP_VEC = 4;
 
-template <class L>
-__global__ void __launch_bounds__(THREADS) clip_kernel(const __grid_constant__ L l, const float* result, int in_place) {
-  const float scale = result[1];
-  if (in_place && scale == 1.f) return;  // g * 1 is g
-  const int total = l.start[l.count];
-  int chunk = blockIdx.x;
-  if (chunk >= total) return;
-  int t = find_tensor(l, chunk);
-  for (; chunk < total; chunk += gridDim.x) {
-    while (l.start[t + 1] <= chunk) ++t;
-    const int dt = l.type[t] & 3, align = l.align[t];
-    const bool f32 = dt == GNS_F32;
-    Unit u[CLIP_UNITS];
-    long long off[CLIP_UNITS][2];
-    int valid[CLIP_UNITS];
-    float x[8];
+template <int DT>
+GNS_DEV void scale_vec(Vec& u, float scale) {
 #pragma unroll
-    for (int k = 0; k < CLIP_UNITS; ++k) {
-      valid[k] = locate<CLIP_UNITS>(l, t, chunk, k * THREADS + static_cast<int>(threadIdx.x), off[k]);
-      load_unit(u[k], l.ptr[0][t], off[k][0], f32, align, valid[k]);
+  for (int e = 0; e < 4; ++e) {
+    if (DT == GNS_F32) {
+      u.w[e] = __float_as_uint(__uint_as_float(u.w[e]) * scale);
+    } else {
+      const float2 x = halves<DT>(u.w[e]);
+      if (DT == GNS_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x * scale, x.y * scale);
+        u.w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __half2 h = __floats2half2_rn(x.x * scale, x.y * scale);
+        u.w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      }
     }
+  }
+}
+
+GNS_DEV void scale_vec(Vec& u, float scale, int dt) {
+  if (dt == GNS_F32)
+    scale_vec<GNS_F32>(u, scale);
+  else if (dt == GNS_BF16)
+    scale_vec<GNS_BF16>(u, scale);
+  else
+    scale_vec<GNS_F16>(u, scale);
+}
+
+// Every block forms the norm from the partial sums (a few KB, in L2), which saves a launch; the
+// chunks go backwards, as the list's end is what the pass for the norm left in L2.
+template <class L>
+__global__ void __launch_bounds__(THREADS, CLIP_BLOCKS) clip_kernel(const __grid_constant__ L l, Finish f, float* result,
+                                                                   int* status, int in_place) {
+  grid_dep_wait();
+  float norm, scale;
+  finish_norm(f, &norm, &scale);
+  if (result && blockIdx.x == 0) write_result(norm, scale, result, status);
+  if (in_place && scale == 1.f) return;  // g * 1 is g
+  int chunk = l.start[l.count] - 1 - static_cast<int>(blockIdx.x);
+  if (chunk < 0) return;
+  int t = find_tensor(l, chunk);
+  for (; chunk >= 0; chunk -= gridDim.x) {
+    while (l.start[t] > chunk) --t;
+    const int dt = l.type[t] & 3, log = vec_log(dt), align = l.align[t];
+    Vec u[CLIP_VEC];
+    long long off[CLIP_VEC][2];
+    int valid[CLIP_VEC];
 #pragma unroll
-    for (int k = 0; k < CLIP_UNITS; ++k) {
-      unpack(x, u[k], dt);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= scale;
-      pack(u[k], x, dt);
-      store_unit(u[k], l.ptr[1][t], off[k][1], f32, align, valid[k]);
+    for (int k = 0; k < CLIP_VEC; ++k) {
+      valid[k] = locate(l, t, chunk, THREADS * CLIP_VEC, log, k * THREADS + static_cast<int>(threadIdx.x), off[k]);
+      load_vec(u[k], l.ptr[0][t], off[k][0], log, align, valid[k]);
     }
     if (static_cast<int>(threadIdx.x) < head_here(l, t, chunk)) {
-      load_unit(u[0], l.ptr[0][t], threadIdx.x, f32, 0, 1);
-      unpack(x, u[0], dt);
-      x[0] *= scale;
-      pack(u[0], x, dt);
-      store_unit(u[0], l.ptr[1][t], threadIdx.x, f32, 0, 1);
+      Vec h;
+      load_vec(h, l.ptr[0][t], threadIdx.x, log, 0, 1);
+      scale_vec(h, scale, dt);
+      store_vec(h, l.ptr[1][t], threadIdx.x, log, 0, 1);
+    }
+#pragma unroll
+    for (int k = 0; k < CLIP_VEC; ++k) {
+      scale_vec(u[k], scale, dt);
+      store_vec(u[k], l.ptr[1][t], off[k][1], log, align, valid[k]);
     }
   }
 }
@@ -511,7 +641,7 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
   for (; chunk < total; chunk += gridDim.x) {
     while (l.start[t + 1] <= chunk) ++t;
     long long off[5];
-    const int valid = locate<1>(l, t, chunk, threadIdx.x, off);
+    const int valid = locate(l, t, chunk, THREADS, 3, threadIdx.x, off);
     if (valid) adamw_at(l, t, off, l.align[t], valid, a, s, &bad);
     if (static_cast<int>(threadIdx.x) < head_here(l, t, chunk)) {
 #pragma unroll
@@ -584,37 +714,48 @@ struct Roles {
   }
 };
 
-// Whether every role of tensor i, `skip` elements in, starts on `bytes(r)`: 8 elements' bytes
-// (level 2) or 16 bytes (level 1).
-bool aligned(const Roles& a, int i, int skip, int level, bool rows) {
-  for (int r = 0; r < a.nroles; ++r) {
-    if (!a.has(r, i)) continue;
-    const gns_tensor& t = a.role[r][i];
-    const int es = size_of(t.dtype), need = level == 2 ? 8 * es : 16;
-    if ((reinterpret_cast<uintptr_t>(t.x.ptr) + static_cast<uintptr_t>(skip) * es) % need) return false;
-    if (rows && t.x.rows > 1 && (t.x.ld * es) % need) return false;
-    if (rows && t.x.count > 1 && (t.x.stride * es) % need) return false;
-  }
-  return true;
-}
-
-// Fills entry k of a launch's list with tensor i; the number of its units of 8 elements.
+// Fills entry k of a launch's list with tensor i; the number of its units of `unit` elements. A
+// unit is one 16-byte vector of the norm and of clipping, and 8 elements of AdamW.
 template <int R, int CAP>
 int64_t put(FlatList<R, CAP>* l, int k, const Roles& a, int i) {
   const gns_batch& x = a.role[0][i].x;
   const int64_t n = x.count * x.rows * x.cols;
+  // elements from each role's first one to the next unit boundary: `wide` counts 8 elements
+  // (16-bit: 16 bytes, f32: 32), `f32_16` 16 bytes of f32
+  int wide = -1, f32_16 = -1, half = -1;
+  bool same_wide = true, same_16 = true;
+  for (int r = 0; r < R; ++r) {
+    if (!a.has(r, i)) continue;
+    const gns_tensor& t = a.role[r][i];
+    const uintptr_t at = reinterpret_cast<uintptr_t>(t.x.ptr);
+    const bool f32 = t.dtype == GNS_F32;
+    const int w = static_cast<int>((0 - (f32 ? at >> 2 : at >> 1)) & 7);
+    if (wide < 0) wide = w;
+    same_wide &= w == wide;
+    int& seen = f32 ? f32_16 : half;
+    const int v = f32 ? w & 3 : w;
+    if (seen < 0) seen = v;
+    same_16 &= seen == v;
+  }
+  const bool vectors = R < 5;
   int head = 0, align = 0;
-  for (int level = 2; level >= 1 && !align; --level)
-    for (int h = 0; h < 8 && !align; ++h)
-      if (aligned(a, i, h, level, false)) {
-        align = level;
-        head = h;
-      }
+  if (vectors) {
+    head = f32_16 >= 0 ? f32_16 : half;
+    align = same_16;
+  } else if (same_wide) {
+    head = wide;
+    align = 2;
+  } else if (same_16 && (half < 0 || f32_16 < 0 || (half & 3) == f32_16)) {
+    head = half >= 0 ? half : f32_16;
+    align = 1;
+  }
+  if (!align) head = 0;
   if (head > n) head = static_cast<int>(n);
   l->n[k] = n;
   l->head[k] = static_cast<unsigned char>(head);
   l->align[k] = static_cast<unsigned char>(align);
-  return std::max<int64_t>(1, (n - head + 7) / 8);
+  const int log = vectors && a.role[0][i].dtype == GNS_F32 ? 2 : 3;
+  return std::max<int64_t>(1, (n - head + (1 << log) - 1) >> log);
 }
 
 template <int R, int CAP>
@@ -623,13 +764,21 @@ int64_t put(RowList<R, CAP>* l, int k, const Roles& a, int i) {
   l->rows[k] = static_cast<int>(x.rows);
   l->nrows[k] = static_cast<int>(x.count * x.rows);
   l->cols[k] = static_cast<int>(x.cols);
+  uint64_t bits16 = 0, bits32 = 0;  // low bits of every address and step in bytes, 16-bit and f32
   for (int r = 0; r < R; ++r) {
-    const bool has = a.has(r, i);
-    l->ld[r][k] = has && a.role[r][i].x.rows > 1 ? a.role[r][i].x.ld : 0;
-    l->stride[r][k] = has && a.role[r][i].x.count > 1 ? a.role[r][i].x.stride : 0;
+    l->ld[r][k] = l->stride[r][k] = 0;
+    if (!a.has(r, i)) continue;
+    const gns_tensor& t = a.role[r][i];
+    if (t.x.rows > 1) l->ld[r][k] = t.x.ld;
+    if (t.x.count > 1) l->stride[r][k] = t.x.stride;
+    const int es = size_of(t.dtype);
+    (es == 4 ? bits32 : bits16) |= reinterpret_cast<uintptr_t>(t.x.ptr) | static_cast<uint64_t>(l->ld[r][k] * es) |
+                                   static_cast<uint64_t>(l->stride[r][k] * es);
   }
-  l->align[k] = static_cast<unsigned char>(aligned(a, i, 0, 2, true) ? 2 : aligned(a, i, 0, 1, true) ? 1 : 0);
-  return x.count * x.rows * ((x.cols + 7) / 8);
+  const bool on16 = ((bits16 | bits32) & 15) == 0;
+  l->align[k] = static_cast<unsigned char>(!on16 ? 0 : (bits32 & 31) ? 1 : 2);
+  const int log = R < 5 && a.role[0][i].dtype == GNS_F32 ? 2 : 3;
+  return x.count * x.rows * ((x.cols + (1 << log) - 1) >> log);
 }
 
 // Collects the tensors with is_flat() == !L::kRows from `from` on, until the list is full or
@@ -675,10 +824,24 @@ int each_list(const Roles& a, int64_t chunk_units, F f) {
   return GNS_OK;
 }
 
-int launched(const char* what) {
+// One launch of THREADS threads a block. behind: the kernel may begin while the one ahead of it
+// on the stream ends, and waits for it itself (grid_dep_wait) before it touches memory.
+template <class... P, class... A>
+int launch(const char* what, void (*kernel)(P...), int grid, void* stream, bool behind, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = &attr;
+  cfg.numAttrs = behind ? 1 : 0;
   profile_count_launch();
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? GNS_OK : set_error(GNS_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e == cudaSuccess) return GNS_OK;
+  (void)cudaGetLastError();
+  return set_error(GNS_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
 int grid_for(int chunks, int per_sm) { return std::max(1, std::min({chunks, device_sm_count() * per_sm, MAX_GRID})); }
@@ -709,27 +872,23 @@ int norm_parts(const gns_tensor* g, int n, int norm_type, float max_norm, float 
   const int inf = norm_type == GNS_NORM_INF;
   const Roles a = {{g}, 1, n};
   auto go = [&](const auto& l) {
-    const int grid = grid_for(l.start[l.count], 8);
-    norm_part_kernel<<<grid, THREADS, 0, static_cast<cudaStream_t>(stream)>>>(l, inf, part + nparts);
+    using L = std::decay_t<decltype(l)>;
+    const int grid = grid_for(l.start[l.count], NORM_BLOCKS);
+    double* at = part + nparts;
     nparts += grid;
-    return launched("grad norm");
+    return launch("grad norm", inf ? norm_part_kernel<true, L> : norm_part_kernel<false, L>, grid, stream, false, l, at);
   };
-  int rc = each_list<FlatList<1, NORM_FLAT>>(a, THREADS * NORM_UNITS, go);
-  if (!rc) rc = each_list<RowList<1, NORM_ROWS>>(a, THREADS * NORM_UNITS, go);
+  int rc = each_list<FlatList<1, NORM_FLAT>>(a, THREADS * NORM_VEC, go);
+  if (!rc) rc = each_list<RowList<1, NORM_ROWS>>(a, THREADS * NORM_VEC, go);
   *f = {part, nparts, inf, max_norm, eps};
   return rc;
-}
-
-int finish_launch(const Finish& f, float* result, int32_t* dev_status, void* stream) {
-  norm_finish_kernel<<<1, THREADS, 0, static_cast<cudaStream_t>(stream)>>>(f, result, dev_status);
-  return launched("grad norm");
 }
 
 int grad_norm(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, float* result, void* ws,
               size_t ws_bytes, int32_t* dev_status, void* stream) {
   Finish f;
   if (int rc = norm_parts(g, n, norm_type, max_norm, eps, result, ws, ws_bytes, stream, &f)) return rc;
-  return finish_launch(f, result, dev_status, stream);
+  return launch("grad norm", norm_finish_kernel, 1, stream, f.nparts > 0, f, result, dev_status);
 }
 
 int clip_grads(const gns_tensor* g, const gns_tensor* out, int n, int norm_type, float max_norm, float eps,
@@ -749,14 +908,18 @@ int clip_grads(const gns_tensor* g, const gns_tensor* out, int n, int norm_type,
   }
   Finish f;
   if (int rc = norm_parts(g, n, norm_type, max_norm, eps, result, ws, ws_bytes, stream, &f)) return rc;
-  if (int rc = finish_launch(f, result, dev_status, stream)) return rc;
+  if (!f.nparts) return launch("clip", norm_finish_kernel, 1, stream, false, f, result, dev_status);
   const Roles a = {{g, out ? out : g}, 2, n};
+  float* write = result;  // by the first launch
   auto go = [&](const auto& l) {
-    clip_kernel<<<grid_for(l.start[l.count], 8), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(l, result, in_place);
-    return launched("clip");
+    using L = std::decay_t<decltype(l)>;
+    const int rc = launch("clip", clip_kernel<L>, grid_for(l.start[l.count], CLIP_BLOCKS), stream, true, l, f, write,
+                          dev_status, in_place);
+    write = nullptr;
+    return rc;
   };
-  int rc = each_list<FlatList<2, CLIP_FLAT>>(a, THREADS * CLIP_UNITS, go);
-  return rc ? rc : each_list<RowList<2, CLIP_ROWS>>(a, THREADS * CLIP_UNITS, go);
+  int rc = each_list<FlatList<2, CLIP_FLAT>>(a, THREADS * CLIP_VEC, go);
+  return rc ? rc : each_list<RowList<2, CLIP_ROWS>>(a, THREADS * CLIP_VEC, go);
 }
 
 int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, const gns_tensor* V,
@@ -805,8 +968,8 @@ int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, co
   a.status = dev_status;
   const Roles lists = {{W, G, M, V, master}, 5, n};
   auto go = [&](const auto& l) {
-    adamw_kernel<<<grid_for(l.start[l.count], 8), THREADS, 0, static_cast<cudaStream_t>(stream)>>>(l, a);
-    return launched("AdamW");
+    using L = std::decay_t<decltype(l)>;
+    return launch("AdamW", adamw_kernel<L>, grid_for(l.start[l.count], 8), stream, false, l, a);
   };
   int rc = each_list<FlatList<5, ADAMW_FLAT>>(lists, THREADS, go);
   return rc ? rc : each_list<RowList<5, ADAMW_ROWS>>(lists, THREADS, go);
