@@ -14,11 +14,13 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <string>
 #include <type_traits>
 
-#include "../../include/gns.h"
+#include "gns.h"
 #include "common.cuh"
 #include "gemm.h"
 
@@ -29,9 +31,18 @@ int set_error(int code, const std::string& msg);  // sets gns_last_error(); defi
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int MAX_GRID = 1216;  // blocks of one norm launch, and its partial sums
+constexpr int MAX_GRID = 1216;  // blocks of one launch at most
+#ifndef LDH
+#define LDH ""
+#endif
+#ifndef NORM_VEC
+#define NORM_VEC 8
+#endif
+#ifndef CLIP_VEC
+#define CLIP_VEC 4
+#endif
 #ifndef NORM_BLOCKS
-#define NORM_BLOCKS 8
+#define NORM_BLOCKS 4
 #endif
 #ifndef CLIP_BLOCKS
 #define CLIP_BLOCKS 4
@@ -44,6 +55,8 @@ constexpr int MAX_GRID = 1216;  // blocks of one norm launch, and its partial su
 // of roles 0 and 1 in bits 0-1 and 2-3, bit 4 set when the tensor has every role.
 template <int R, int CAP>
 struct FlatList {
+  template <int C>
+  using Cap = FlatList<R, C>;
   static constexpr bool kRows = false;
   static constexpr int kRoles = R, kCap = CAP;
   void* ptr[R][CAP];
@@ -57,6 +70,8 @@ struct FlatList {
 
 template <int R, int CAP>
 struct RowList {
+  template <int C>
+  using Cap = RowList<R, C>;
   static constexpr bool kRows = true;
   static constexpr int kRoles = R, kCap = CAP;
   void* ptr[R][CAP];
@@ -64,6 +79,8 @@ struct RowList {
   int rows[CAP];   // of one matrix
   int nrows[CAP];  // of all matrices
   int cols[CAP];
+  // 2^64 / d + 1 for the units of a row and the rows of a matrix (0: d is 1)
+  unsigned long long by_row[CAP], by_matrix[CAP];
   int start[CAP + 1];
   unsigned char type[CAP];
   unsigned char align[CAP];
@@ -78,7 +95,7 @@ struct Unit {
 };
 
 GNS_DEV void ld_v8(uint32_t (&w)[8], const void* p) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+  asm volatile("ld.global" LDH ".v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                : "l"(p)
                : "memory");
@@ -89,7 +106,7 @@ GNS_DEV void st_v8(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 GNS_DEV void ld_v4(uint32_t* w, const void* p) {
-  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global" LDH ".v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                : "l"(p)
                : "memory");
@@ -217,36 +234,49 @@ GNS_DEV int locate(const FlatList<R, CAP>& l, int t, int chunk, int per, int log
 #pragma unroll
   for (int r = 0; r < R; ++r) off[r] = o;
   const long long left = l.n[t] - o, most = 1 << log;
-  return static_cast<int>(max(0ll, min(left, most)));
+  const int valid = static_cast<int>(max(0ll, min(left, most)));
+  return l.align[t] && valid < most ? 0 : valid;  // what is left of a unit is an edge
+}
+
+// x / d by a product with inv = 2^64 / d + 1 (0 for d = 1): exact for 32-bit x and d, as
+// x < 2^32 times inv's error, below 1, stays under 2^64 / d. Dividing costs the rows' kernels
+// more than everything else they do with a vector.
+GNS_DEV uint32_t quotient(uint32_t x, unsigned long long inv) {
+  return inv ? static_cast<uint32_t>(__umul64hi(x, inv)) : x;
 }
 
 template <int R, int CAP>
 GNS_DEV int locate(const RowList<R, CAP>& l, int t, int chunk, int per, int log, int j, long long (&off)[R]) {
   const uint32_t cols = static_cast<uint32_t>(l.cols[t]), width = 1u << log;
   const uint32_t per_row = (cols + width - 1u) >> log;
-  const long long u0 = static_cast<long long>(chunk - l.start[t]) * per;
-  const long long row0 = u0 / per_row;
+  const unsigned long long u0 = static_cast<unsigned long long>(chunk - l.start[t]) * per;
+  // the chunk's first row; a tensor of 2^32 units or more has it by a division
+  const unsigned long long row0 = (u0 >> 32) == 0 ? quotient(static_cast<uint32_t>(u0), l.by_row[t]) : u0 / per_row;
   const uint32_t x = static_cast<uint32_t>(u0 - row0 * per_row) + static_cast<uint32_t>(j);
-  const uint32_t q = x / per_row;
-  const long long row = row0 + q;
+  const uint32_t q = quotient(x, l.by_row[t]);
+  const unsigned long long row = row0 + q;
   if (row >= l.nrows[t]) return 0;
   const uint32_t c = (x - q * per_row) << log;
-  const uint32_t b = static_cast<uint32_t>(row) / static_cast<uint32_t>(l.rows[t]);
+  const uint32_t b = quotient(static_cast<uint32_t>(row), l.by_matrix[t]);
   const uint32_t i = static_cast<uint32_t>(row) - b * static_cast<uint32_t>(l.rows[t]);
 #pragma unroll
   for (int r = 0; r < R; ++r) off[r] = b * l.stride[r][t] + i * l.ld[r][t] + c;
   return static_cast<int>(min(width, cols - c));
 }
 
-// Elements before the first unit of a flat tensor: one for each of the first threads of its
-// first chunk, where `head_here` is the number of them.
+// The edges of a flat tensor that starts on a unit boundary only `head` elements in: the elements
+// before its first unit and after its last whole one. The first threads of its first chunk take
+// one each. Returns this thread's, or -1.
 template <int R, int CAP>
-GNS_DEV int head_here(const FlatList<R, CAP>& l, int t, int chunk) {
-  return chunk == l.start[t] ? l.head[t] : 0;
+GNS_DEV long long edge(const FlatList<R, CAP>& l, int t, int chunk, int log) {
+  if (chunk != l.start[t] || !l.align[t]) return -1;
+  const int i = threadIdx.x, head = l.head[t];
+  const int tail = static_cast<int>((l.n[t] - head) & ((1 << log) - 1));
+  return i < head ? i : i < head + tail ? l.n[t] - tail + (i - head) : -1;
 }
 template <int R, int CAP>
-GNS_DEV int head_here(const RowList<R, CAP>&, int, int) {
-  return 0;
+GNS_DEV long long edge(const RowList<R, CAP>&, int, int, int) {
+  return -1;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -331,32 +361,56 @@ GNS_DEV float2 halves(uint32_t w) {
 // ---------------------------------------------------------------------------------------
 // norm: sqrt(sum x^2) over the whole list, or max |x|
 
-constexpr int NORM_VEC = 4;
+
+
+// Loads this thread's N vectors of a chunk (vector k * THREADS + threadIdx.x is its k-th), those
+// beyond the last whole one as zeros. Nearly every chunk is whole: its loads go out with nothing
+// to work out for each. One role is always aligned.
+template <int N, int CAP>
+GNS_DEV void load_chunk(const FlatList<1, CAP>& l, int t, int chunk, int log, Vec (&u)[N]) {
+  const long long o = l.head[t] + (static_cast<long long>(chunk - l.start[t]) * (THREADS * N) << log);
+  const long long left = (l.n[t] - o) >> log;
+  const char* p = static_cast<const char*>(l.ptr[0][t]) + (o << (4 - log)) + threadIdx.x * 16;
+  if (left >= THREADS * N) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * THREADS * 16);
+  } else {
+    const int n = static_cast<int>(left);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      u[k] = {};
+      if (k * THREADS + static_cast<int>(threadIdx.x) < n) ld_v4(u[k].w, p + k * THREADS * 16);
+    }
+  }
+}
+
+template <int N, int CAP>
+GNS_DEV void load_chunk(const RowList<1, CAP>& l, int t, int chunk, int log, Vec (&u)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    long long off[1];
+    const int valid = locate(l, t, chunk, THREADS * N, log, k * THREADS + static_cast<int>(threadIdx.x), off);
+    load_vec(u[k], l.ptr[0][t], off[0], log, l.align[t], valid);
+  }
+}
 
 // Calls f(vectors, type) for this block's chunks, NORM_VEC vectors a thread at a time.
 template <class L, class F>
 GNS_DEV void for_vectors(const L& l, F f) {
   const int total = l.start[l.count];
-  int chunk = blockIdx.x;
-  if (chunk >= total) return;
+  int chunk = static_cast<int>(static_cast<long long>(total) * blockIdx.x / gridDim.x);
+  const int end = static_cast<int>(static_cast<long long>(total) * (blockIdx.x + 1) / gridDim.x);
+  if (chunk >= end) return;
   int t = find_tensor(l, chunk);
-  for (; chunk < total; chunk += gridDim.x) {
+  for (; chunk < end; ++chunk) {
     while (l.start[t + 1] <= chunk) ++t;
-    const int dt = l.type[t] & 3, log = vec_log(dt), align = l.align[t];
-    const void* p = l.ptr[0][t];
-    Vec u[NORM_VEC];
-#pragma unroll
-    for (int k = 0; k < NORM_VEC; ++k) {
-      long long off[1];
-      const int valid = locate(l, t, chunk, THREADS * NORM_VEC, log, k * THREADS + static_cast<int>(threadIdx.x), off);
-      load_vec(u[k], p, off[0], log, align, valid);
-    }
-    if (static_cast<int>(threadIdx.x) < head_here(l, t, chunk)) {
-      Vec h[NORM_VEC] = {};
-      load_vec(h[0], p, threadIdx.x, log, 0, 1);
-      f(h, dt);
-    }
+    const int dt = l.type[t] & 3, log = vec_log(dt);
+    Vec u[NORM_VEC], h[NORM_VEC] = {};
+    const long long e = edge(l, t, chunk, log);
+    if (e >= 0) load_vec(h[0], l.ptr[0][t], e, log, 0, 1);
+    load_chunk(l, t, chunk, log, u);
     f(u, dt);
+    if (e >= 0) f(h, dt);
   }
 }
 
@@ -401,7 +455,95 @@ GNS_DEV double sum_squares(const L& l, float pre, uint32_t* bits) {
   return s;
 }
 
-// part[blockIdx.x] = the block's sum of squares (INF = false) or largest magnitude (INF = true).
+// A block's partial sum, and the number of the call that it belongs to: written and read as one
+// 16-byte access, so whoever sees the number sees the sum.
+struct alignas(16) Slot {
+  double value;
+  unsigned long long call;
+};
+
+GNS_DEV void put_slot(Slot* s, double value, unsigned long long call) {
+  asm volatile(
+      "{\n\t.reg .b128 x;\n\tmov.b128 x, {%1, %2};\n\tst.relaxed.gpu.global.b128 [%0], x;\n\t}" ::"l"(s),
+      "l"(__double_as_longlong(value)), "l"(call)
+      : "memory");
+}
+
+GNS_DEV Slot get_slot(const Slot* s) {
+  long long v;
+  Slot r;
+  asm volatile("{\n\t.reg .b128 x;\n\tld.relaxed.gpu.global.b128 x, [%2];\n\tmov.b128 {%0, %1}, x;\n\t}"
+               : "=l"(v), "=l"(r.call)
+               : "l"(s)
+               : "memory");
+  r.value = __longlong_as_double(v);
+  return r;
+}
+
+// What a norm call leaves in result[0] and result[1], from the slots of its launches.
+struct Finish {
+  Slot* slots;
+  unsigned long long call;
+  float* result;
+  int* status;
+  int nslots;
+  int inf;
+  float max_norm;  // infinity: no clipping
+  float eps;
+};
+
+// The norm and the scale, in every thread of the block, from slots that hold this call's sums
+// (WAIT = false) or will do so (WAIT = true), added in a fixed order. Waiting ends after
+// GNS_WAIT_TIMEOUT_NS at the latest, with a NaN and the timeout bit.
+template <bool WAIT>
+GNS_DEV void finish_norm(const Finish& f, float* norm, float* scale) {
+  __shared__ float out[2];
+  double n = 0.0;
+  uint32_t m = 0;
+  for (int i = threadIdx.x; i < f.nslots; i += THREADS) {
+    Slot s = get_slot(f.slots + i);
+    if (WAIT) {
+      uint64_t t0 = 0;
+      for (uint32_t k = 1; s.call != f.call; ++k) {
+        if ((k & 63u) == 0u) {
+          const uint64_t now = global_timer_ns();
+          if (!t0) t0 = now;
+          if (now - t0 > GNS_WAIT_TIMEOUT_NS) {
+            set_status(f.status, GNS_DEVST_TIMEOUT);
+            s.value = __longlong_as_double(0x7ff8000000000000ll);
+            break;
+          }
+        }
+        s = get_slot(f.slots + i);
+      }
+      put_slot(f.slots + i, 0.0, 0);  // a replay of the captured call writes the same number again
+    }
+    n += s.value;
+    m = max(m, __float_as_uint(static_cast<float>(s.value)));
+  }
+  n = f.inf ? static_cast<double>(__uint_as_float(block_max(m))) : block_sum(n);
+  if (threadIdx.x == 0) {
+    if (!f.inf) n = sqrt(n);
+    out[0] = static_cast<float>(n);
+    const double c = static_cast<double>(f.max_norm) / (n + static_cast<double>(f.eps));
+    out[1] = isinf(f.max_norm) || c >= 1.0 ? 1.f : static_cast<float>(c);  // a NaN norm gives a NaN scale
+  }
+  __syncthreads();
+  *norm = out[0];
+  *scale = out[1];
+}
+
+GNS_DEV void write_result(const Finish& f, float norm, float scale) {
+  if (threadIdx.x == 0) {
+    f.result[0] = norm;
+    f.result[1] = scale;
+    if (!isfinite(norm)) set_status(f.status, GNS_DEVST_NONFINITE);
+  }
+}
+
+// slots[blockIdx.x] = the block's sum of squares (INF = false) or largest magnitude (INF = true).
+// Where the call needs no further launch the last block then gathers all slots (`finish`): no
+// block waits for that one, so it may wait for them whatever the order in which they run.
 //
 // Squares of f32 and bf16 values leave f32's range long before the values do (above 2^64, below
 // 2^-63). A block whose sum says that this has happened (it is not finite, or below 2^-80 though
@@ -409,8 +551,10 @@ GNS_DEV double sum_squares(const L& l, float pre, uint32_t* bits) {
 // every value that counts: the largest magnitudes become at most 2^28, and where the sum lies
 // below 2^-80 none is above 2^-40, so they become at most 2^60. f64 holds the result.
 template <bool INF, class L>
-__global__ void __launch_bounds__(THREADS, NORM_BLOCKS) norm_part_kernel(const __grid_constant__ L l, double* part) {
+__global__ void __launch_bounds__(THREADS, NORM_BLOCKS) norm_kernel(const __grid_constant__ L l, Slot* slots, Finish f,
+                                                                   int finish) {
   grid_dep_launch();
+  double s;
   if (INF) {
     uint32_t m = 0;  // magnitudes order as their bits do, with every NaN above infinity
     for_vectors(l, [&](const Vec (&u)[NORM_VEC], int dt) {
@@ -427,71 +571,35 @@ __global__ void __launch_bounds__(THREADS, NORM_BLOCKS) norm_part_kernel(const _
           }
         }
     });
-    m = block_max(m);
-    if (threadIdx.x == 0) part[blockIdx.x] = static_cast<double>(__uint_as_float(m));
-    return;
-  }
-  uint32_t bits = 0;
-  double s = block_sum(sum_squares<false>(l, 1.f, &bits));
-  const int any = __syncthreads_or(bits != 0);
-  if (!(s <= 1e38))
-    s = block_sum(sum_squares<true>(l, 0x1p-100f, &bits)) * 0x1p200;
-  else if (s < 0x1p-80 && any)
-    s = block_sum(sum_squares<true>(l, 0x1p100f, &bits)) * 0x1p-200;
-  if (threadIdx.x == 0) part[blockIdx.x] = s;
-}
-
-// What a norm call leaves in result[0] and result[1], from its partial sums.
-struct Finish {
-  const double* part;
-  int nparts;
-  int inf;
-  float max_norm;  // infinity: no clipping
-  float eps;
-};
-
-// The norm and the scale, in every thread of the block.
-GNS_DEV void finish_norm(const Finish& f, float* norm, float* scale) {
-  __shared__ float out[2];
-  double n = 0.0;
-  if (f.inf) {
-    uint32_t m = 0;
-    for (int i = threadIdx.x; i < f.nparts; i += THREADS) m = max(m, __float_as_uint(static_cast<float>(f.part[i])));
-    n = static_cast<double>(__uint_as_float(block_max(m)));
+    s = static_cast<double>(__uint_as_float(block_max(m)));
   } else {
-    for (int i = threadIdx.x; i < f.nparts; i += THREADS) n += f.part[i];
-    n = block_sum(n);
+    uint32_t bits = 0;
+    s = block_sum(sum_squares<false>(l, 1.f, &bits));
+    const int any = __syncthreads_or(bits != 0);
+    if (!(s <= 1e38))
+      s = block_sum(sum_squares<true>(l, 0x1p-100f, &bits)) * 0x1p200;
+    else if (s < 0x1p-80 && any)
+      s = block_sum(sum_squares<true>(l, 0x1p100f, &bits)) * 0x1p-200;
   }
-  if (threadIdx.x == 0) {
-    if (!f.inf) n = sqrt(n);
-    out[0] = static_cast<float>(n);
-    const double c = static_cast<double>(f.max_norm) / (n + static_cast<double>(f.eps));
-    out[1] = isinf(f.max_norm) || c >= 1.0 ? 1.f : static_cast<float>(c);  // a NaN norm gives a NaN scale
-  }
-  __syncthreads();
-  *norm = out[0];
-  *scale = out[1];
-}
-
-GNS_DEV void write_result(float norm, float scale, float* result, int* status) {
-  if (threadIdx.x == 0) {
-    result[0] = norm;
-    result[1] = scale;
-    if (!isfinite(norm)) set_status(status, GNS_DEVST_NONFINITE);
+  if (threadIdx.x == 0) put_slot(slots + blockIdx.x, s, f.call);
+  if (finish && blockIdx.x == gridDim.x - 1) {
+    float norm, scale;
+    finish_norm<true>(f, &norm, &scale);
+    write_result(f, norm, scale);
   }
 }
 
-__global__ void __launch_bounds__(THREADS) norm_finish_kernel(Finish f, float* result, int* status) {
-  grid_dep_wait();
+// A list of empty tensors.
+__global__ void __launch_bounds__(THREADS) no_norm_kernel(Finish f) {
   float norm, scale;
-  finish_norm(f, &norm, &scale);
-  write_result(norm, scale, result, status);
+  finish_norm<false>(f, &norm, &scale);
+  write_result(f, norm, scale);
 }
 
 // ---------------------------------------------------------------------------------------
 // clipping: out = round(scale * g); roles: gradient, output (the same pointers in place)
 
-constexpr int CLIP_VEC = 4;
+
 
 template <int DT>
 GNS_DEV void scale_vec(Vec& u, float scale) {
@@ -521,41 +629,80 @@ GNS_DEV void scale_vec(Vec& u, float scale, int dt) {
     scale_vec<GNS_F16>(u, scale);
 }
 
+// Scales one chunk of tensor t.
+template <int CAP>
+GNS_DEV void clip_chunk(const FlatList<2, CAP>& l, int t, int chunk, int dt, float scale) {
+  const int log = vec_log(dt);
+  const long long o = l.head[t] + (static_cast<long long>(chunk - l.start[t]) * (THREADS * CLIP_VEC) << log);
+  Vec u[CLIP_VEC];
+  if (l.align[t]) {
+    const long long left = (l.n[t] - o) >> log;
+    const long long at = (o << (4 - log)) + threadIdx.x * 16;
+    const char* p = static_cast<const char*>(l.ptr[0][t]) + at;
+    char* q = static_cast<char*>(l.ptr[1][t]) + at;
+    const int n = static_cast<int>(min(left, static_cast<long long>(THREADS * CLIP_VEC))) - static_cast<int>(threadIdx.x);
+#pragma unroll
+    for (int k = 0; k < CLIP_VEC; ++k)
+      if (k * THREADS < n) ld_v4(u[k].w, p + k * THREADS * 16);
+#pragma unroll
+    for (int k = 0; k < CLIP_VEC; ++k)
+      if (k * THREADS < n) {
+        scale_vec(u[k], scale, dt);
+        st_v4(q + k * THREADS * 16, u[k].w);
+      }
+    return;
+  }
+  // gradient and output can not both be on 16 bytes: neighbouring threads take neighbouring elements
+  const int n = static_cast<int>(min(l.n[t] - o, static_cast<long long>(THREADS * CLIP_VEC << log)));
+  for (int i = threadIdx.x; i < n; i += THREADS) {
+    load_vec(u[0], l.ptr[0][t], o + i, log, 0, 1);
+    scale_vec(u[0], scale, dt);
+    store_vec(u[0], l.ptr[1][t], o + i, log, 0, 1);
+  }
+}
+
+template <int CAP>
+GNS_DEV void clip_chunk(const RowList<2, CAP>& l, int t, int chunk, int dt, float scale) {
+  const int log = vec_log(dt);
+  Vec u[CLIP_VEC];
+  long long off[CLIP_VEC][2];
+  int valid[CLIP_VEC];
+#pragma unroll
+  for (int k = 0; k < CLIP_VEC; ++k) {
+    valid[k] = locate(l, t, chunk, THREADS * CLIP_VEC, log, k * THREADS + static_cast<int>(threadIdx.x), off[k]);
+    load_vec(u[k], l.ptr[0][t], off[k][0], log, l.align[t], valid[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < CLIP_VEC; ++k) {
+    scale_vec(u[k], scale, dt);
+    store_vec(u[k], l.ptr[1][t], off[k][1], log, l.align[t], valid[k]);
+  }
+}
+
 // Every block forms the norm from the partial sums (a few KB, in L2), which saves a launch; the
 // chunks go backwards, as the list's end is what the pass for the norm left in L2.
 template <class L>
-__global__ void __launch_bounds__(THREADS, CLIP_BLOCKS) clip_kernel(const __grid_constant__ L l, Finish f, float* result,
-                                                                   int* status, int in_place) {
+__global__ void __launch_bounds__(THREADS, CLIP_BLOCKS) clip_kernel(const __grid_constant__ L l, Finish f, int first,
+                                                                   int in_place) {
   grid_dep_wait();
   float norm, scale;
-  finish_norm(f, &norm, &scale);
-  if (result && blockIdx.x == 0) write_result(norm, scale, result, status);
+  finish_norm<false>(f, &norm, &scale);
+  if (first && blockIdx.x == 0) write_result(f, norm, scale);
   if (in_place && scale == 1.f) return;  // g * 1 is g
   int chunk = l.start[l.count] - 1 - static_cast<int>(blockIdx.x);
   if (chunk < 0) return;
   int t = find_tensor(l, chunk);
   for (; chunk >= 0; chunk -= gridDim.x) {
     while (l.start[t] > chunk) --t;
-    const int dt = l.type[t] & 3, log = vec_log(dt), align = l.align[t];
-    Vec u[CLIP_VEC];
-    long long off[CLIP_VEC][2];
-    int valid[CLIP_VEC];
-#pragma unroll
-    for (int k = 0; k < CLIP_VEC; ++k) {
-      valid[k] = locate(l, t, chunk, THREADS * CLIP_VEC, log, k * THREADS + static_cast<int>(threadIdx.x), off[k]);
-      load_vec(u[k], l.ptr[0][t], off[k][0], log, align, valid[k]);
-    }
-    if (static_cast<int>(threadIdx.x) < head_here(l, t, chunk)) {
+    const int dt = l.type[t] & 3;
+    const long long e = edge(l, t, chunk, vec_log(dt));
+    if (e >= 0) {
       Vec h;
-      load_vec(h, l.ptr[0][t], threadIdx.x, log, 0, 1);
+      load_vec(h, l.ptr[0][t], e, vec_log(dt), 0, 1);
       scale_vec(h, scale, dt);
-      store_vec(h, l.ptr[1][t], threadIdx.x, log, 0, 1);
+      store_vec(h, l.ptr[1][t], e, vec_log(dt), 0, 1);
     }
-#pragma unroll
-    for (int k = 0; k < CLIP_VEC; ++k) {
-      scale_vec(u[k], scale, dt);
-      store_vec(u[k], l.ptr[1][t], off[k][1], log, align, valid[k]);
-    }
+    clip_chunk(l, t, chunk, dt, scale);
   }
 }
 
@@ -643,9 +790,10 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
     long long off[5];
     const int valid = locate(l, t, chunk, THREADS, 3, threadIdx.x, off);
     if (valid) adamw_at(l, t, off, l.align[t], valid, a, s, &bad);
-    if (static_cast<int>(threadIdx.x) < head_here(l, t, chunk)) {
+    const long long e = edge(l, t, chunk, 3);
+    if (e >= 0) {
 #pragma unroll
-      for (int r = 0; r < 5; ++r) off[r] = threadIdx.x;
+      for (int r = 0; r < 5; ++r) off[r] = e;
       adamw_at(l, t, off, 0, 1, a, s, &bad);
     }
   }
@@ -755,8 +903,11 @@ int64_t put(FlatList<R, CAP>* l, int k, const Roles& a, int i) {
   l->head[k] = static_cast<unsigned char>(head);
   l->align[k] = static_cast<unsigned char>(align);
   const int log = vectors && a.role[0][i].dtype == GNS_F32 ? 2 : 3;
-  return std::max<int64_t>(1, (n - head + (1 << log) - 1) >> log);
+  // an aligned tensor's last elements, less than a unit, are an edge of its first chunk
+  return std::max<int64_t>(1, (n - head + (align ? 0 : (1 << log) - 1)) >> log);
 }
+
+uint64_t inverse(int64_t d) { return d > 1 ? ~uint64_t(0) / static_cast<uint64_t>(d) + 1 : 0; }
 
 template <int R, int CAP>
 int64_t put(RowList<R, CAP>* l, int k, const Roles& a, int i) {
@@ -778,7 +929,10 @@ int64_t put(RowList<R, CAP>* l, int k, const Roles& a, int i) {
   const bool on16 = ((bits16 | bits32) & 15) == 0;
   l->align[k] = static_cast<unsigned char>(!on16 ? 0 : (bits32 & 31) ? 1 : 2);
   const int log = R < 5 && a.role[0][i].dtype == GNS_F32 ? 2 : 3;
-  return x.count * x.rows * ((x.cols + (1 << log) - 1) >> log);
+  const int64_t per_row = (x.cols + (1 << log) - 1) >> log;
+  l->by_row[k] = inverse(per_row);
+  l->by_matrix[k] = inverse(x.rows);
+  return x.count * x.rows * per_row;
 }
 
 // Collects the tensors with is_flat() == !L::kRows from `from` on, until the list is full or
@@ -805,15 +959,23 @@ int fill(L* l, const Roles& a, int from, int64_t chunk_units) {
 }
 
 // Lists of one launch: how many tensors its parameters hold.
-constexpr int NORM_FLAT = 1024, NORM_ROWS = 512, CLIP_FLAT = 768, CLIP_ROWS = 384, ADAMW_FLAT = 512, ADAMW_ROWS = 192;
+#ifndef SMALL
+#define SMALL 64
+#endif
+constexpr int SMALL_LIST = SMALL;
+constexpr int NORM_FLAT = 1024, NORM_ROWS = 448, CLIP_FLAT = 768, CLIP_ROWS = 320, ADAMW_FLAT = 512, ADAMW_ROWS = 176;
 
 static_assert(sizeof(FlatList<1, NORM_FLAT>) < 32000 && sizeof(RowList<1, NORM_ROWS>) < 32000, "kernel parameters");
 static_assert(sizeof(FlatList<2, CLIP_FLAT>) < 32000 && sizeof(RowList<2, CLIP_ROWS>) < 32000, "kernel parameters");
 static_assert(sizeof(FlatList<5, ADAMW_FLAT>) < 32000 && sizeof(RowList<5, ADAMW_ROWS>) < 32000, "kernel parameters");
 
-// Launches f(list) for every launch that the tensors of one layout need.
+// Launches f(list) for every launch that the tensors of one layout need. A short list goes with
+// short parameters (SMALL_LIST).
 template <class L, class F>
 int each_list(const Roles& a, int64_t chunk_units, F f) {
+  if constexpr (L::kCap > SMALL_LIST) {
+    if (a.n <= SMALL_LIST) return each_list<typename L::template Cap<SMALL_LIST>>(a, chunk_units, f);
+  }
   L l;
   for (int i = 0; i < a.n;) {
     i = fill(&l, a, i, chunk_units);
@@ -849,12 +1011,26 @@ int grid_for(int chunks, int per_sm) { return std::max(1, std::min({chunks, devi
 size_t list_workspace(int n) {
   // at most one launch for every full list of each layout, and one more of each
   const size_t launches = static_cast<size_t>(n) / NORM_FLAT + static_cast<size_t>(n) / NORM_ROWS + 2;
-  return launches * MAX_GRID * sizeof(double) + 256;
+  return launches * MAX_GRID * sizeof(Slot) + 256;
 }
 
-// The checks and the partial sums of a norm call; *f is ready for the kernel that finishes it.
-int norm_parts(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, float* result, void* ws,
-               size_t ws_bytes, void* stream, Finish* f) {
+// A number for a norm call that no other call has, and that memory a workspace is made from does
+// not hold but by a chance of 2^-64: a mix of a counter that is a bijection of 64 bits (the finalizer
+// of SplitMix64, Steele, Lea and Flood 2014).
+uint64_t call_number() {
+  static const uint64_t seed = static_cast<uint64_t>(std::chrono::high_resolution_clock::now().time_since_epoch().count());
+  static std::atomic<uint64_t> calls{0};
+  uint64_t z = (seed << 20) + ++calls;
+  z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
+  z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
+  z ^= z >> 31;
+  return z ? z : 1;
+}
+
+// The checks and launches of a norm; finish: result is written too. *f names the slots for a
+// later launch.
+int norm(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, float* result, void* ws, size_t ws_bytes,
+         int32_t* dev_status, void* stream, bool finish, Finish* f) {
   if (!g || !result) return set_error(GNS_ERR_INVALID, "null argument");
   if (n < 1) return set_error(GNS_ERR_INVALID, "need at least one tensor");
   if (norm_type != GNS_NORM_L2 && norm_type != GNS_NORM_INF) return set_error(GNS_ERR_INVALID, "unknown norm type");
@@ -867,28 +1043,30 @@ int norm_parts(const gns_tensor* g, int n, int norm_type, float max_norm, float 
   if (reinterpret_cast<uintptr_t>(ws) % 256) return set_error(GNS_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   if (ws_bytes < list_workspace(n))
     return set_error(GNS_ERR_WORKSPACE, "workspace too small: need " + std::to_string(list_workspace(n)) + " bytes");
-  double* part = static_cast<double*>(ws);
-  int nparts = 0;
   const int inf = norm_type == GNS_NORM_INF;
+  *f = {static_cast<Slot*>(ws), call_number(), result, dev_status, 0, inf, max_norm, eps};
   const Roles a = {{g}, 1, n};
+  int left = 0;  // tensors that no launch has taken yet
+  for (int i = 0; i < n; ++i) left += !empty(g[i]);
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
     const int grid = grid_for(l.start[l.count], NORM_BLOCKS);
-    double* at = part + nparts;
-    nparts += grid;
-    return launch("grad norm", inf ? norm_part_kernel<true, L> : norm_part_kernel<false, L>, grid, stream, false, l, at);
+    Slot* at = f->slots + f->nslots;
+    f->nslots += grid;
+    left -= l.count;
+    return launch("grad norm", inf ? norm_kernel<true, L> : norm_kernel<false, L>, grid, stream, false, l, at, *f,
+                  static_cast<int>(finish && !left));
   };
+  if (!left && finish) return launch("grad norm", no_norm_kernel, 1, stream, false, *f);
   int rc = each_list<FlatList<1, NORM_FLAT>>(a, THREADS * NORM_VEC, go);
   if (!rc) rc = each_list<RowList<1, NORM_ROWS>>(a, THREADS * NORM_VEC, go);
-  *f = {part, nparts, inf, max_norm, eps};
   return rc;
 }
 
 int grad_norm(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, float* result, void* ws,
               size_t ws_bytes, int32_t* dev_status, void* stream) {
   Finish f;
-  if (int rc = norm_parts(g, n, norm_type, max_norm, eps, result, ws, ws_bytes, stream, &f)) return rc;
-  return launch("grad norm", norm_finish_kernel, 1, stream, f.nparts > 0, f, result, dev_status);
+  return norm(g, n, norm_type, max_norm, eps, result, ws, ws_bytes, dev_status, stream, true, &f);
 }
 
 int clip_grads(const gns_tensor* g, const gns_tensor* out, int n, int norm_type, float max_norm, float eps,
@@ -907,15 +1085,14 @@ int clip_grads(const gns_tensor* g, const gns_tensor* out, int n, int norm_type,
       return fail(GNS_ERR_INVALID, "outs", i, "may alias its gradient only with the same layout");
   }
   Finish f;
-  if (int rc = norm_parts(g, n, norm_type, max_norm, eps, result, ws, ws_bytes, stream, &f)) return rc;
-  if (!f.nparts) return launch("clip", norm_finish_kernel, 1, stream, false, f, result, dev_status);
+  if (int rc = norm(g, n, norm_type, max_norm, eps, result, ws, ws_bytes, dev_status, stream, false, &f)) return rc;
+  if (!f.nslots) return launch("clip", no_norm_kernel, 1, stream, false, f);
   const Roles a = {{g, out ? out : g}, 2, n};
-  float* write = result;  // by the first launch
+  int first = 1;  // the launch that writes the result
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
-    const int rc = launch("clip", clip_kernel<L>, grid_for(l.start[l.count], CLIP_BLOCKS), stream, true, l, f, write,
-                          dev_status, in_place);
-    write = nullptr;
+    const int rc = launch("clip", clip_kernel<L>, grid_for(l.start[l.count], CLIP_BLOCKS), stream, true, l, f, first, in_place);
+    first = 0;
     return rc;
   };
   int rc = each_list<FlatList<2, CLIP_FLAT>>(a, THREADS * CLIP_VEC, go);

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence, Union
 
@@ -21,30 +22,42 @@ import torch
 from . import _lib
 from ._lib import GnsAdamwParams, GnsTensor, load
 from ._lib import check as check_rc
-from .api import _CallStatus, _dtype_code, _stream_ptr, alloc_workspace
+from .api import _CallStatus, _dtype_code, alloc_workspace
 
 
-def _describe(e: GnsTensor, t: torch.Tensor):
-    """Fills the descriptor of one tensor; returns what has to agree between the roles of an
-    operator: its shape, and the order of its dimensions in memory unless that is the usual."""
+# Field by field a descriptor costs ten times what one packed write does.
+_PACK = struct.Struct("PqqqqqiI").pack_into
+assert struct.calcsize("PqqqqqiI") == ctypes.sizeof(GnsTensor)
+_CODES = {torch.bfloat16: _lib.GNS_BF16, torch.float16: _lib.GNS_F16, torch.float32: _lib.GNS_F32}
+
+
+def _describe(array, at: int, t: torch.Tensor):
+    """Writes the descriptor of one tensor at byte `at`; returns what has to agree between the
+    roles of an operator: its shape, and the order of its dimensions in memory unless that is the
+    usual."""
     if not t.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
-    e.dtype = _dtype_code(t)
-    e.x.ptr = t.data_ptr()
+    code = _CODES.get(t.dtype)
+    if code is None:
+        code = _dtype_code(t)  # says what is supported
     shape = tuple(t.shape)
+    n = len(shape)
     if t.is_contiguous():
-        if len(shape) <= 1:
-            count, rows, cols = 1, 1, t.numel()
-        elif len(shape) == 2:
-            count, (rows, cols) = 1, shape
+        if n == 1:
+            _PACK(array, at, t.data_ptr(), 1, 1, shape[0], shape[0], shape[0], code, 0)
+        elif n == 2:
+            rows, cols = shape
+            _PACK(array, at, t.data_ptr(), 1, rows, cols, cols, rows * cols, code, 0)
+        elif n == 0:
+            _PACK(array, at, t.data_ptr(), 1, 1, 1, 1, 1, code, 0)
         else:
-            count, rows, cols = math.prod(shape[:-2]), shape[-2], shape[-1]
-        e.x.count, e.x.rows, e.x.cols, e.x.ld, e.x.stride = count, rows, cols, cols, rows * cols
+            rows, cols = shape[-2:]
+            _PACK(array, at, t.data_ptr(), math.prod(shape[:-2]), rows, cols, cols, rows * cols, code, 0)
         return shape
-    order = tuple(sorted(range(len(shape)), key=lambda d: (-t.stride(d), -shape[d], d)))
+    order = tuple(sorted(range(n), key=lambda d: (-t.stride(d), -shape[d], d)))
     u = t.permute(order)
     if u.is_contiguous():
-        _describe(e, u)
+        _describe(array, at, u)
         return shape, order
     # leading dimensions that lie evenly behind one another are one
     dims, steps = list(shape), list(t.stride())
@@ -60,7 +73,7 @@ def _describe(e: GnsTensor, t: torch.Tensor):
             count > 1 and stride < (rows - 1) * ld * (rows > 1) + cols):
         raise ValueError(f"a tensor of shape {shape} with strides {tuple(t.stride())} is neither without gaps nor a "
                          "batch of rows with a contiguous last dimension: make it contiguous")
-    e.x.count, e.x.rows, e.x.cols, e.x.ld, e.x.stride = count, rows, cols, max(ld, cols), stride
+    _PACK(array, at, t.data_ptr(), count, rows, cols, max(ld, cols), stride, code, 0)
     return shape
 
 
@@ -77,19 +90,21 @@ class TensorList:
         self.address = ctypes.addressof(self.array)
         self.device = None
         layout = []
-        for e, t in zip(self.array, self.tensors):
+        array, size, at = self.array, ctypes.sizeof(GnsTensor), 0
+        for t in self.tensors:
             if t is None:
                 layout.append(None)
-                continue
-            layout.append(_describe(e, t))
-            if self.device is None:
-                self.device = t.device
-            elif self.device != t.device:
-                raise ValueError("the tensors of a list must live on one device")
+            else:
+                layout.append(_describe(array, at, t))
+                if self.device is None:
+                    self.device = t.device
+                elif self.device != t.device:
+                    raise ValueError("the tensors of a list must live on one device")
+            at += size
         self.has_none = None in layout
-        # compared as text: two lists of hundreds of tensors in a fraction of a microsecond
         self.layout = layout
-        self.layout_text = repr(layout)
+        self.layout_key = hash(tuple(layout))  # two lists of hundreds of tensors compare at once
+        self.reordered = any(x is not None and x and type(x[0]) is tuple for x in layout)
 
     def __len__(self):
         return len(self.tensors)
@@ -102,9 +117,15 @@ def tensor_list(tensors: Union[TensorList, torch.Tensor, Sequence[Optional[torch
     return TensorList([tensors] if isinstance(tensors, torch.Tensor) else tensors)
 
 
+def _stream(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
+    """The stream's handle; for the device's current one without building a Stream object, which
+    takes as long as a launch."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _same_layout(name: str, a: TensorList, b: TensorList, optional: bool = False) -> None:
-    if a.layout_text == b.layout_text:
-        return
+    if a.layout_key == b.layout_key or (optional and not a.reordered and not b.reordered and len(a) == len(b)):
+        return  # the library compares the shapes itself: what it cannot see is the order in memory
     if len(a) != len(b):
         raise ValueError(f"{name}: {len(b)} tensors, expected {len(a)}")
     for i, (x, y) in enumerate(zip(a.layout, b.layout)):
@@ -160,7 +181,7 @@ def grad_norm(grads, max_norm: Optional[float] = None, norm_type: float = 2.0, e
     result, ws = _norm_buffers(g, result, workspace, stream)
     cs = _CallStatus(status, g.device, check, stream)
     rc = load().gns_grad_norm(g.address, len(g), code, math.inf if max_norm is None else float(max_norm), float(eps),
-                              result.data_ptr(), ws.data_ptr(), ws.numel(), cs.ptr(), _stream_ptr(stream, g.device))
+                              result.data_ptr(), ws.data_ptr(), ws.numel(), cs.ptr(), _stream(stream, g.device))
     check_rc(rc, "gns_grad_norm")
     cs.done("gns_grad_norm")
     return result
@@ -181,7 +202,7 @@ def clip_grads(grads, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6
     result, ws = _norm_buffers(g, result, workspace, stream)
     cs = _CallStatus(status, g.device, check, stream)
     rc = load().gns_clip_grads(g.address, out_address, len(g), code, float(max_norm), float(eps), result.data_ptr(),
-                               ws.data_ptr(), ws.numel(), cs.ptr(), _stream_ptr(stream, g.device))
+                               ws.data_ptr(), ws.numel(), cs.ptr(), _stream(stream, g.device))
     check_rc(rc, "gns_clip_grads")
     cs.done("gns_clip_grads")
     return result
@@ -243,6 +264,6 @@ def adamw_step(W, G, M, V, lr: Optional[float] = None, beta1: float = 0.9, beta2
     rc = load().gns_adamw_step(w.address, g.address, m.address, v.address, master_address, len(w),
                                ctypes.byref(params.c_struct()), _device_scalar("grad_scale", grad_scale, torch.float32),
                                _device_scalar("step_count", step_count, torch.int32), cs.ptr(),
-                               _stream_ptr(stream, w.device))
+                               _stream(stream, w.device))
     check_rc(rc, "gns_adamw_step")
     cs.done("gns_adamw_step")
