@@ -31,6 +31,16 @@ int set_error(int code, const std::string& msg);  // sets gns_last_error(); defi
 namespace {
 
 constexpr int THREADS = 256;
+
+// The threads that take a chunk together: a block of THREADS, or a warp.
+struct Block {
+  static constexpr int kThreads = THREADS;
+  GNS_DEV static int rank() { return threadIdx.x; }
+};
+struct Warp {
+  static constexpr int kThreads = 32;
+  GNS_DEV static int rank() { return threadIdx.x & 31; }
+};
 constexpr int MAX_GRID = 1216;  // blocks of one launch at most
 #ifndef LDH
 #define LDH ""
@@ -267,43 +277,45 @@ GNS_DEV int locate(const RowList<R, CAP>& l, int t, int chunk, int per, int log,
 // The edges of a flat tensor that starts on a unit boundary only `head` elements in: the elements
 // before its first unit and after its last whole one. The first threads of its first chunk take
 // one each. Returns this thread's, or -1.
-template <int R, int CAP>
+template <class T, int R, int CAP>
 GNS_DEV long long edge(const FlatList<R, CAP>& l, int t, int chunk, int log) {
   if (chunk != l.start[t] || !l.align[t]) return -1;
-  const int i = threadIdx.x, head = l.head[t];
+  const int i = T::rank(), head = l.head[t];
   const int tail = static_cast<int>((l.n[t] - head) & ((1 << log) - 1));
   return i < head ? i : i < head + tail ? l.n[t] - tail + (i - head) : -1;
 }
-template <int R, int CAP>
+template <class T, int R, int CAP>
 GNS_DEV long long edge(const RowList<R, CAP>&, int, int, int) {
   return -1;
 }
 
 // ---------------------------------------------------------------------------------------
-// reductions over a block, in a fixed order; every thread gets the result
+// reductions over a block of BT threads, in a fixed order; every thread gets the result
 
-GNS_DEV double block_sum(double v) {
-  __shared__ double part[THREADS / 32];
+template <int BT>
+GNS_DEV float block_sum(float v) {
+  __shared__ float part[BT / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
-  double s = 0.0;
+  float s = 0.f;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) s += part[w];
+  for (int w = 0; w < BT / 32; ++w) s += part[w];
   return s;
 }
 
+template <int BT>
 GNS_DEV uint32_t block_max(uint32_t v) {
-  __shared__ uint32_t part[THREADS / 32];
+  __shared__ uint32_t part[BT / 32];
   v = __reduce_max_sync(0xffffffffu, v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   uint32_t m = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) m = max(m, part[w]);
+  for (int w = 0; w < BT / 32; ++w) m = max(m, part[w]);
   return m;
 }
 
@@ -363,52 +375,65 @@ GNS_DEV float2 halves(uint32_t w) {
 
 
 
-// Loads this thread's N vectors of a chunk (vector k * THREADS + threadIdx.x is its k-th), those
-// beyond the last whole one as zeros. Nearly every chunk is whole: its loads go out with nothing
-// to work out for each. One role is always aligned.
-template <int N, int CAP>
-GNS_DEV void load_chunk(const FlatList<1, CAP>& l, int t, int chunk, int log, Vec (&u)[N]) {
-  const long long o = l.head[t] + (static_cast<long long>(chunk - l.start[t]) * (THREADS * N) << log);
-  const long long left = (l.n[t] - o) >> log;
-  const char* p = static_cast<const char*>(l.ptr[0][t]) + (o << (4 - log)) + threadIdx.x * 16;
-  if (left >= THREADS * N) {
+// Loads this thread's N vectors of a chunk (of a group of W threads, vector k * W + rank is its
+// k-th), those beyond the last whole one as zeros. Nearly every chunk is whole: its loads go out
+// with nothing to work out for each. The one role that counts here, the gradients, is aligned
+// unless it shares its head with an output that is not.
+template <class T, int N, int R, int CAP>
+GNS_DEV void load_chunk(const FlatList<R, CAP>& l, int t, int chunk, int log, Vec (&u)[N]) {
+  constexpr int W = T::kThreads;
+  const long long o = l.head[t] + (static_cast<long long>(chunk - l.start[t]) * (W * N) << log);
+  if (R == 1 || l.align[t]) {
+    const long long left = (l.n[t] - o) >> log;
+    const char* p = static_cast<const char*>(l.ptr[0][t]) + (o << (4 - log)) + T::rank() * 16;
+    if (left >= W * N) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * THREADS * 16);
+      for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
+    } else {
+      const int n = static_cast<int>(left);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        u[k] = {};
+        if (k * W + T::rank() < n) ld_v4(u[k].w, p + k * W * 16);
+      }
+    }
   } else {
-    const int n = static_cast<int>(left);
+    const int n = static_cast<int>(min(l.n[t] - o, static_cast<long long>(W * N << log)));
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      u[k] = {};
-      if (k * THREADS + static_cast<int>(threadIdx.x) < n) ld_v4(u[k].w, p + k * THREADS * 16);
+      const int at = (k * W + T::rank()) << log;
+      load_vec(u[k], l.ptr[0][t], o + at, log, 0, max(0, min(n - at, 1 << log)));
     }
   }
 }
 
-template <int N, int CAP>
-GNS_DEV void load_chunk(const RowList<1, CAP>& l, int t, int chunk, int log, Vec (&u)[N]) {
+template <class T, int N, int R, int CAP>
+GNS_DEV void load_chunk(const RowList<R, CAP>& l, int t, int chunk, int log, Vec (&u)[N]) {
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    long long off[1];
-    const int valid = locate(l, t, chunk, THREADS * N, log, k * THREADS + static_cast<int>(threadIdx.x), off);
+    long long off[R];
+    const int valid = locate(l, t, chunk, T::kThreads * N, log, k * T::kThreads + T::rank(), off);
     load_vec(u[k], l.ptr[0][t], off[0], log, l.align[t], valid);
   }
 }
 
-// Calls f(vectors, type) for this block's chunks, NORM_VEC vectors a thread at a time.
-template <class L, class F>
-GNS_DEV void for_vectors(const L& l, F f) {
+// Calls f(vectors, type) for this thread's vectors, N of a chunk at a time. The groups of T
+// threads of the launch (this one is `group` of `groups`) have one run of the chunks each: a run
+// crosses few tensors, where a stride over the list crosses many at each step.
+template <class T, int N, class L, class F>
+GNS_DEV void for_vectors(const L& l, int group, int groups, F f) {
   const int total = l.start[l.count];
-  int chunk = static_cast<int>(static_cast<long long>(total) * blockIdx.x / gridDim.x);
-  const int end = static_cast<int>(static_cast<long long>(total) * (blockIdx.x + 1) / gridDim.x);
+  int chunk = static_cast<int>(static_cast<long long>(total) * group / groups);
+  const int end = static_cast<int>(static_cast<long long>(total) * (group + 1) / groups);
   if (chunk >= end) return;
   int t = find_tensor(l, chunk);
   for (; chunk < end; ++chunk) {
     while (l.start[t + 1] <= chunk) ++t;
     const int dt = l.type[t] & 3, log = vec_log(dt);
-    Vec u[NORM_VEC], h[NORM_VEC] = {};
-    const long long e = edge(l, t, chunk, log);
+    Vec u[N], h[N] = {};
+    const long long e = edge<T>(l, t, chunk, log);
     if (e >= 0) load_vec(h[0], l.ptr[0][t], e, log, 0, 1);
-    load_chunk(l, t, chunk, log, u);
+    load_chunk<T>(l, t, chunk, log, u);
     f(u, dt);
     if (e >= 0) f(h, dt);
   }
@@ -416,11 +441,11 @@ GNS_DEV void for_vectors(const L& l, F f) {
 
 // f32 sum of the squares of a thread's vectors of one chunk, the values scaled by `pre` first
 // (SCALED).
-template <int DT, bool SCALED>
-GNS_DEV float squares(const Vec (&u)[NORM_VEC], float pre) {
+template <int DT, bool SCALED, int N>
+GNS_DEV float squares(const Vec (&u)[N], float pre) {
   float q[2] = {0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < NORM_VEC; ++k)
+  for (int k = 0; k < N; ++k)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (DT == GNS_F32) {
@@ -436,47 +461,94 @@ GNS_DEV float squares(const Vec (&u)[NORM_VEC], float pre) {
   return q[0] + q[1];
 }
 
-// Sum of squares over this block's chunks: a thread's up to 32 squares of a chunk in f32, these
-// sums in f64 (one conversion and one sum a chunk: at one for each 8 squares the f64 pipe bounds
-// the kernel).
-template <bool SCALED, class L>
-GNS_DEV double sum_squares(const L& l, float pre, uint32_t* bits) {
-  double s = 0.0;
-  for_vectors(l, [&](const Vec (&u)[NORM_VEC], int dt) {
+// Sum of this thread's squares: up to 64 of a chunk in f32, these sums with the rounding error of
+// each addition kept beside them (Knuth's two-sum), as f32 holds too little for a long list and
+// f64, at 2 operations a clock and SM, took longer than the loads.
+template <bool SCALED, class T, int N, class L>
+GNS_DEV float sum_squares(const L& l, int group, int groups, float pre, uint32_t* bits) {
+  float s = 0.f, lost = 0.f;
+  for_vectors<T, N>(l, group, groups, [&](const Vec (&u)[N], int dt) {
     const float q = dt == GNS_F32    ? squares<GNS_F32, SCALED>(u, pre)
                     : dt == GNS_BF16 ? squares<GNS_BF16, SCALED>(u, pre)
                                      : squares<GNS_F16, SCALED>(u, pre);
-    s += static_cast<double>(q);
+    const float t = __fadd_rn(s, q), b = __fsub_rn(t, s);
+    lost += __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(q, b));
+    s = t;
     if (!SCALED) {
 #pragma unroll
-      for (int k = 0; k < NORM_VEC; ++k) *bits |= (u[k].w[0] | u[k].w[1]) | (u[k].w[2] | u[k].w[3]);
+      for (int k = 0; k < N; ++k) *bits |= (u[k].w[0] | u[k].w[1]) | (u[k].w[2] | u[k].w[3]);
     }
   });
-  return s;
+  return isfinite(s) ? s + lost : s;
 }
 
-// A block's partial sum, and the number of the call that it belongs to: written and read as one
-// 16-byte access, so whoever sees the number sees the sum.
+// A share m 2^e of a sum of squares, e = 0, 200 or -200; or a magnitude m, e = 0.
+struct Share {
+  float m;
+  int e;
+};
+
+// This block's share of the norm, in every thread: its sum of squares or (INF) its largest
+// magnitude.
+//
+// Squares of f32 and bf16 values leave f32's range long before the values do (above 2^64, below
+// 2^-63). A block whose sum says that this may have happened (it is above 2^100 or not finite, or
+// below 2^-80 though some bit is set) sums once more with the values scaled by 2^-100 or 2^100,
+// which is exact for every value that counts: the largest magnitudes become at most 2^28, and
+// where the sum lies below 2^-80 none is above 2^-40, so they become at most 2^60.
+template <bool INF, class T, int N, int BT, class L>
+GNS_DEV Share block_share(const L& l, int group, int groups) {
+  if (INF) {
+    uint32_t m = 0;  // magnitudes order as their bits do, with every NaN above infinity
+    for_vectors<T, N>(l, group, groups, [&](const Vec (&u)[N], int dt) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = u[k].w[e];
+          if (dt == GNS_F32) {
+            m = max(m, w & 0x7fffffffu);
+          } else {
+            const float2 x = dt == GNS_BF16 ? halves<GNS_BF16>(w) : halves<GNS_F16>(w);
+            m = max(m, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
+          }
+        }
+    });
+    return {__uint_as_float(block_max<BT>(m)), 0};
+  }
+  uint32_t bits = 0;
+  const float s = block_sum<BT>(sum_squares<false, T, N>(l, group, groups, 1.f, &bits));
+  const int any = __syncthreads_or(bits != 0);
+  if (!(s <= 0x1p100f)) return {block_sum<BT>(sum_squares<true, T, N>(l, group, groups, 0x1p-100f, &bits)), 200};
+  if (s < 0x1p-80f && any) return {block_sum<BT>(sum_squares<true, T, N>(l, group, groups, 0x1p100f, &bits)), -200};
+  return {s, 0};
+}
+
+// A block's share, and the number of the call that it belongs to: written and read as one 16-byte
+// access, so whoever sees the number sees the share.
 struct alignas(16) Slot {
-  double value;
+  Share share;
   unsigned long long call;
 };
 
-GNS_DEV void put_slot(Slot* s, double value, unsigned long long call) {
+GNS_DEV void put_slot(Slot* s, Share v, unsigned long long call) {
   asm volatile(
-      "{\n\t.reg .b128 x;\n\tmov.b128 x, {%1, %2};\n\tst.relaxed.gpu.global.b128 [%0], x;\n\t}" ::"l"(s),
-      "l"(__double_as_longlong(value)), "l"(call)
+      "{\n\t.reg .b128 x;\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tmov.b128 x, {v, %3};\n\t"
+      "st.relaxed.gpu.global.b128 [%0], x;\n\t}" ::"l"(s),
+      "r"(__float_as_uint(v.m)), "r"(v.e), "l"(call)
       : "memory");
 }
 
 GNS_DEV Slot get_slot(const Slot* s) {
-  long long v;
+  uint32_t m;
   Slot r;
-  asm volatile("{\n\t.reg .b128 x;\n\tld.relaxed.gpu.global.b128 x, [%2];\n\tmov.b128 {%0, %1}, x;\n\t}"
-               : "=l"(v), "=l"(r.call)
-               : "l"(s)
-               : "memory");
-  r.value = __longlong_as_double(v);
+  asm volatile(
+      "{\n\t.reg .b128 x;\n\t.reg .b64 v;\n\tld.relaxed.gpu.global.b128 x, [%3];\n\tmov.b128 {v, %2}, x;\n\t"
+      "mov.b64 {%0, %1}, v;\n\t}"
+      : "=r"(m), "=r"(r.share.e), "=l"(r.call)
+      : "l"(s)
+      : "memory");
+  r.share.m = __uint_as_float(m);
   return r;
 }
 
@@ -492,14 +564,30 @@ struct Finish {
   float eps;
 };
 
-// The norm and the scale, in every thread of the block, from slots that hold this call's sums
+// Shares are added as they are where all have e = 0, which nearly always they do. Otherwise the
+// sum has the largest exponent of those that are not zero: a share with the next one is then a
+// float still, one two further down is too small to count.
+GNS_DEV uint32_t exponents(Share s) { return s.m == 0.f ? 0u : s.e < 0 ? 1u : s.e == 0 ? 2u : 4u; }
+GNS_DEV int top_exponent(uint32_t seen) { return seen & 4u ? 200 : seen & 2u || !seen ? 0 : -200; }
+GNS_DEV float scaled_share(Share s, int top) {
+  return s.e == top ? s.m : s.e + 200 == top ? s.m * 0x1p-100f * 0x1p-100f : 0.f;
+}
+
+// The results from the sum of squares n 2^e, or the largest magnitude n. A NaN norm gives a NaN
+// scale.
+GNS_DEV void norm_and_scale(const Finish& f, float n, int e, float* norm, float* scale) {
+  *norm = f.inf ? n : sqrtf(n) * (e > 0 ? 0x1p100f : e < 0 ? 0x1p-100f : 1.f);
+  const float d = *norm + f.eps;
+  *scale = isinf(f.max_norm) || d <= f.max_norm ? 1.f : f.max_norm / d;
+}
+
+// The norm and the scale, in every thread of the block, from slots that hold this call's shares
 // (WAIT = false) or will do so (WAIT = true), added in a fixed order. Waiting ends after
 // GNS_WAIT_TIMEOUT_NS at the latest, with a NaN and the timeout bit.
 template <bool WAIT>
 GNS_DEV void finish_norm(const Finish& f, float* norm, float* scale) {
-  __shared__ float out[2];
-  double n = 0.0;
-  uint32_t m = 0;
+  uint32_t most = 0, seen = 0;
+  float n = 0.f;
   for (int i = threadIdx.x; i < f.nslots; i += THREADS) {
     Slot s = get_slot(f.slots + i);
     if (WAIT) {
@@ -510,27 +598,33 @@ GNS_DEV void finish_norm(const Finish& f, float* norm, float* scale) {
           if (!t0) t0 = now;
           if (now - t0 > GNS_WAIT_TIMEOUT_NS) {
             set_status(f.status, GNS_DEVST_TIMEOUT);
-            s.value = __longlong_as_double(0x7ff8000000000000ll);
+            s.share = {__int_as_float(0x7fffffff), 0};
+            put_slot(f.slots + i, s.share, f.call);
             break;
           }
         }
         s = get_slot(f.slots + i);
       }
-      put_slot(f.slots + i, 0.0, 0);  // a replay of the captured call writes the same number again
     }
-    n += s.value;
-    m = max(m, __float_as_uint(static_cast<float>(s.value)));
+    most = max(most, __float_as_uint(s.share.m));
+    n += s.share.m;
+    seen |= exponents(s.share);
   }
-  n = f.inf ? static_cast<double>(__uint_as_float(block_max(m))) : block_sum(n);
-  if (threadIdx.x == 0) {
-    if (!f.inf) n = sqrt(n);
-    out[0] = static_cast<float>(n);
-    const double c = static_cast<double>(f.max_norm) / (n + static_cast<double>(f.eps));
-    out[1] = isinf(f.max_norm) || c >= 1.0 ? 1.f : static_cast<float>(c);  // a NaN norm gives a NaN scale
+  int top = 0;
+  if (f.inf) {
+    n = __uint_as_float(block_max<THREADS>(most));
+  } else if (__syncthreads_or((seen & ~2u) != 0)) {
+    seen = (__syncthreads_or((seen & 4u) != 0) ? 4u : 0u) | (__syncthreads_or((seen & 2u) != 0) ? 2u : 0u) | 1u;
+    top = top_exponent(seen);
+    n = 0.f;
+    for (int i = threadIdx.x; i < f.nslots; i += THREADS) n += scaled_share(get_slot(f.slots + i).share, top);
+    n = block_sum<THREADS>(n);
+  } else {
+    n = block_sum<THREADS>(n);
   }
-  __syncthreads();
-  *norm = out[0];
-  *scale = out[1];
+  if (WAIT)  // a replay of the captured call writes the same number again
+    for (int i = threadIdx.x; i < f.nslots; i += THREADS) put_slot(f.slots + i, {0.f, 0}, 0);
+  norm_and_scale(f, n, top, norm, scale);
 }
 
 GNS_DEV void write_result(const Finish& f, float norm, float scale) {
@@ -541,46 +635,14 @@ GNS_DEV void write_result(const Finish& f, float norm, float scale) {
   }
 }
 
-// slots[blockIdx.x] = the block's sum of squares (INF = false) or largest magnitude (INF = true).
-// Where the call needs no further launch the last block then gathers all slots (`finish`): no
-// block waits for that one, so it may wait for them whatever the order in which they run.
-//
-// Squares of f32 and bf16 values leave f32's range long before the values do (above 2^64, below
-// 2^-63). A block whose sum says that this has happened (it is not finite, or below 2^-80 though
-// some bit is set) sums once more with the values scaled by 2^-100 or 2^100, which is exact for
-// every value that counts: the largest magnitudes become at most 2^28, and where the sum lies
-// below 2^-80 none is above 2^-40, so they become at most 2^60. f64 holds the result.
+// slots[blockIdx.x] = the block's share. Where the call needs no further launch the last block
+// then gathers all slots (`finish`): no block waits for that one, so it may wait for them
+// whatever the order in which they run.
 template <bool INF, class L>
 __global__ void __launch_bounds__(THREADS, NORM_BLOCKS) norm_kernel(const __grid_constant__ L l, Slot* slots, Finish f,
                                                                    int finish) {
   grid_dep_launch();
-  double s;
-  if (INF) {
-    uint32_t m = 0;  // magnitudes order as their bits do, with every NaN above infinity
-    for_vectors(l, [&](const Vec (&u)[NORM_VEC], int dt) {
-#pragma unroll
-      for (int k = 0; k < NORM_VEC; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t w = u[k].w[e];
-          if (dt == GNS_F32) {
-            m = max(m, w & 0x7fffffffu);
-          } else {
-            const float2 x = dt == GNS_BF16 ? halves<GNS_BF16>(w) : halves<GNS_F16>(w);
-            m = max(m, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
-          }
-        }
-    });
-    s = static_cast<double>(__uint_as_float(block_max(m)));
-  } else {
-    uint32_t bits = 0;
-    s = block_sum(sum_squares<false>(l, 1.f, &bits));
-    const int any = __syncthreads_or(bits != 0);
-    if (!(s <= 1e38))
-      s = block_sum(sum_squares<true>(l, 0x1p-100f, &bits)) * 0x1p200;
-    else if (s < 0x1p-80 && any)
-      s = block_sum(sum_squares<true>(l, 0x1p100f, &bits)) * 0x1p-200;
-  }
+  const Share s = block_share<INF, Block, NORM_VEC, THREADS>(l, blockIdx.x, gridDim.x);
   if (threadIdx.x == 0) put_slot(slots + blockIdx.x, s, f.call);
   if (finish && blockIdx.x == gridDim.x - 1) {
     float norm, scale;
@@ -629,53 +691,83 @@ GNS_DEV void scale_vec(Vec& u, float scale, int dt) {
     scale_vec<GNS_F16>(u, scale);
 }
 
-// Scales one chunk of tensor t.
-template <int CAP>
+// Scales one chunk of tensor t, N vectors a thread of the group.
+template <class T, int N, int CAP>
 GNS_DEV void clip_chunk(const FlatList<2, CAP>& l, int t, int chunk, int dt, float scale) {
+  constexpr int W = T::kThreads;
   const int log = vec_log(dt);
-  const long long o = l.head[t] + (static_cast<long long>(chunk - l.start[t]) * (THREADS * CLIP_VEC) << log);
-  Vec u[CLIP_VEC];
+  const long long o = l.head[t] + (static_cast<long long>(chunk - l.start[t]) * (W * N) << log);
+  Vec u[N];
   if (l.align[t]) {
     const long long left = (l.n[t] - o) >> log;
-    const long long at = (o << (4 - log)) + threadIdx.x * 16;
+    const long long at = (o << (4 - log)) + T::rank() * 16;
     const char* p = static_cast<const char*>(l.ptr[0][t]) + at;
     char* q = static_cast<char*>(l.ptr[1][t]) + at;
-    const int n = static_cast<int>(min(left, static_cast<long long>(THREADS * CLIP_VEC))) - static_cast<int>(threadIdx.x);
+    if (left >= W * N) {
 #pragma unroll
-    for (int k = 0; k < CLIP_VEC; ++k)
-      if (k * THREADS < n) ld_v4(u[k].w, p + k * THREADS * 16);
+      for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
 #pragma unroll
-    for (int k = 0; k < CLIP_VEC; ++k)
-      if (k * THREADS < n) {
+      for (int k = 0; k < N; ++k) {
         scale_vec(u[k], scale, dt);
-        st_v4(q + k * THREADS * 16, u[k].w);
+        st_v4(q + k * W * 16, u[k].w);
       }
+    } else {
+      const int n = static_cast<int>(left) - T::rank();
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k * W < n) ld_v4(u[k].w, p + k * W * 16);
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k * W < n) {
+          scale_vec(u[k], scale, dt);
+          st_v4(q + k * W * 16, u[k].w);
+        }
+    }
     return;
   }
   // gradient and output can not both be on 16 bytes: neighbouring threads take neighbouring elements
-  const int n = static_cast<int>(min(l.n[t] - o, static_cast<long long>(THREADS * CLIP_VEC << log)));
-  for (int i = threadIdx.x; i < n; i += THREADS) {
+  const int n = static_cast<int>(min(l.n[t] - o, static_cast<long long>(W * N << log)));
+  for (int i = T::rank(); i < n; i += W) {
     load_vec(u[0], l.ptr[0][t], o + i, log, 0, 1);
     scale_vec(u[0], scale, dt);
     store_vec(u[0], l.ptr[1][t], o + i, log, 0, 1);
   }
 }
 
-template <int CAP>
+template <class T, int N, int CAP>
 GNS_DEV void clip_chunk(const RowList<2, CAP>& l, int t, int chunk, int dt, float scale) {
   const int log = vec_log(dt);
-  Vec u[CLIP_VEC];
-  long long off[CLIP_VEC][2];
-  int valid[CLIP_VEC];
+  Vec u[N];
+  long long off[N][2];
+  int valid[N];
 #pragma unroll
-  for (int k = 0; k < CLIP_VEC; ++k) {
-    valid[k] = locate(l, t, chunk, THREADS * CLIP_VEC, log, k * THREADS + static_cast<int>(threadIdx.x), off[k]);
+  for (int k = 0; k < N; ++k) {
+    valid[k] = locate(l, t, chunk, T::kThreads * N, log, k * T::kThreads + T::rank(), off[k]);
     load_vec(u[k], l.ptr[0][t], off[k][0], log, l.align[t], valid[k]);
   }
 #pragma unroll
-  for (int k = 0; k < CLIP_VEC; ++k) {
+  for (int k = 0; k < N; ++k) {
     scale_vec(u[k], scale, dt);
     store_vec(u[k], l.ptr[1][t], off[k][1], log, l.align[t], valid[k]);
+  }
+}
+
+// Scales chunk, chunk - step, ... down to `end`.
+template <class T, int N, class L>
+GNS_DEV void clip_chunks(const L& l, int chunk, int end, int step, float scale) {
+  if (chunk < end) return;
+  int t = find_tensor(l, chunk);
+  for (; chunk >= end; chunk -= step) {
+    while (l.start[t] > chunk) --t;
+    const int dt = l.type[t] & 3;
+    const long long e = edge<T>(l, t, chunk, vec_log(dt));
+    if (e >= 0) {
+      Vec h;
+      load_vec(h, l.ptr[0][t], e, vec_log(dt), 0, 1);
+      scale_vec(h, scale, dt);
+      store_vec(h, l.ptr[1][t], e, vec_log(dt), 0, 1);
+    }
+    clip_chunk<T, N>(l, t, chunk, dt, scale);
   }
 }
 
@@ -689,20 +781,45 @@ __global__ void __launch_bounds__(THREADS, CLIP_BLOCKS) clip_kernel(const __grid
   finish_norm<false>(f, &norm, &scale);
   if (first && blockIdx.x == 0) write_result(f, norm, scale);
   if (in_place && scale == 1.f) return;  // g * 1 is g
-  int chunk = l.start[l.count] - 1 - static_cast<int>(blockIdx.x);
-  if (chunk < 0) return;
-  int t = find_tensor(l, chunk);
-  for (; chunk >= 0; chunk -= gridDim.x) {
-    while (l.start[t] > chunk) --t;
-    const int dt = l.type[t] & 3;
-    const long long e = edge(l, t, chunk, vec_log(dt));
-    if (e >= 0) {
-      Vec h;
-      load_vec(h, l.ptr[0][t], e, vec_log(dt), 0, 1);
-      scale_vec(h, scale, dt);
-      store_vec(h, l.ptr[1][t], e, vec_log(dt), 0, 1);
-    }
-    clip_chunk(l, t, chunk, dt, scale);
+  clip_chunks<Block, CLIP_VEC>(l, l.start[l.count] - 1 - static_cast<int>(blockIdx.x), 0, gridDim.x, scale);
+}
+
+// ---------------------------------------------------------------------------------------
+// short lists: the whole call in one launch of one cluster
+
+// A chunk is 2 KB here, for a warp, so that a list of small tensors spreads over many warps; the
+// blocks' shares meet in shared memory. Compared with the kernels above this saves the slots'
+// way through L2 and, in clipping, a launch; one cluster streams 1 MB in about the time of that.
+constexpr int SHORT_THREADS = 512, SHORT_VEC = 4, SHORT_CLUSTER = 8, SHORT_CHUNKS = 512;
+
+template <bool INF, bool CLIP, class L>
+__global__ void __launch_bounds__(SHORT_THREADS) short_kernel(const __grid_constant__ L l, Finish f, int in_place) {
+  __shared__ alignas(8) Share share[SHORT_CLUSTER];
+  constexpr int warps = SHORT_THREADS / 32;
+  const int blocks = gridDim.x, group = blockIdx.x * warps + (threadIdx.x >> 5), groups = blocks * warps;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const Share s = block_share<INF, Warp, SHORT_VEC, SHORT_THREADS>(l, group, groups);
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every block of the cluster runs
+  if (static_cast<int>(threadIdx.x) < blocks) {
+    const uint32_t to = mapa_shared(smem_u32(&share[blockIdx.x]), threadIdx.x);
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(__float_as_uint(s.m)), "r"(s.e) : "memory");
+  }
+  cluster_sync_all();
+  uint32_t most = 0, seen = 0;
+  for (int b = 0; b < blocks; ++b) {
+    most = max(most, __float_as_uint(share[b].m));
+    seen |= exponents(share[b]);
+  }
+  const int top = top_exponent(seen);
+  float n = 0.f, norm, scale;
+  for (int b = 0; b < blocks; ++b) n += scaled_share(share[b], top);
+  norm_and_scale(f, INF ? __uint_as_float(most) : n, INF ? 0 : top, &norm, &scale);
+  if (blockIdx.x == 0) write_result(f, norm, scale);
+  if constexpr (CLIP) {
+    if (in_place && scale == 1.f) return;
+    const int total = l.start[l.count];  // the run of chunks that this warp has read
+    clip_chunks<Warp, SHORT_VEC>(l, static_cast<int>(static_cast<long long>(total) * (group + 1) / groups) - 1,
+                                 static_cast<int>(static_cast<long long>(total) * group / groups), 1, scale);
   }
 }
 
@@ -790,7 +907,7 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
     long long off[5];
     const int valid = locate(l, t, chunk, THREADS, 3, threadIdx.x, off);
     if (valid) adamw_at(l, t, off, l.align[t], valid, a, s, &bad);
-    const long long e = edge(l, t, chunk, 3);
+    const long long e = edge<Block>(l, t, chunk, 3);
     if (e >= 0) {
 #pragma unroll
       for (int r = 0; r < 5; ++r) off[r] = e;
@@ -986,19 +1103,28 @@ int each_list(const Roles& a, int64_t chunk_units, F f) {
   return GNS_OK;
 }
 
-// One launch of THREADS threads a block. behind: the kernel may begin while the one ahead of it
-// on the stream ends, and waits for it itself (grid_dep_wait) before it touches memory.
+// ALONE: an ordinary launch of THREADS threads a block. BEHIND: one that may begin while the one
+// ahead of it on the stream ends, and waits for it itself (grid_dep_wait) before it touches memory.
+// CLUSTER: one cluster of SHORT_THREADS threads a block.
+enum How { ALONE, BEHIND, CLUSTER };
+
 template <class... P, class... A>
-int launch(const char* what, void (*kernel)(P...), int grid, void* stream, bool behind, const A&... args) {
+int launch(const char* what, void (*kernel)(P...), int grid, void* stream, How how, const A&... args) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr = {};
+  if (how == CLUSTER) {
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = grid;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  } else {
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(how == CLUSTER ? SHORT_THREADS : THREADS);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = &attr;
-  cfg.numAttrs = behind ? 1 : 0;
+  cfg.numAttrs = how == ALONE ? 0 : 1;
   profile_count_launch();
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e == cudaSuccess) return GNS_OK;
@@ -1014,6 +1140,35 @@ size_t list_workspace(int n) {
   return launches * MAX_GRID * sizeof(Slot) + 256;
 }
 
+// Makes the call with f(list) where the list is short: every tensor in one launch's list, of one
+// layout, and few enough chunks. Returns 1 where it is not.
+template <class L, class F>
+int short_list(const Roles& a, int tensors, F f) {
+  L l;
+  fill(&l, a, 0, 32 * SHORT_VEC);
+  return l.count == tensors && l.start[l.count] <= SHORT_CHUNKS ? f(l) : 1;
+}
+
+template <int R, class F>
+int short_lists(const Roles& a, int tensors, F f) {
+  if (a.n > SMALL_LIST) return 1;
+  int64_t total = 0;
+  for (int i = 0; i < a.n; ++i) {
+    const gns_tensor& t = a.role[0][i];
+    total += t.x.count * t.x.rows * t.x.cols * size_of(t.dtype);
+    if (total > SHORT_CHUNKS * 2048) return 1;
+  }
+  const int rc = short_list<FlatList<R, SMALL_LIST>>(a, tensors, f);
+  return rc <= 0 ? rc : short_list<RowList<R, SMALL_LIST>>(a, tensors, f);
+}
+
+// Blocks of the cluster: one for each `warps` chunks, a power of two.
+int short_blocks(int chunks) {
+  int blocks = 1;
+  while (blocks < SHORT_CLUSTER && blocks * (SHORT_THREADS / 32) < chunks) blocks *= 2;
+  return blocks;
+}
+
 // A number for a norm call that no other call has, and that memory a workspace is made from does
 // not hold but by a chance of 2^-64: a mix of a counter that is a bijection of 64 bits (the finalizer
 // of SplitMix64, Steele, Lea and Flood 2014).
@@ -1027,10 +1182,8 @@ uint64_t call_number() {
   return z ? z : 1;
 }
 
-// The checks and launches of a norm; finish: result is written too. *f names the slots for a
-// later launch.
-int norm(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, float* result, void* ws, size_t ws_bytes,
-         int32_t* dev_status, void* stream, bool finish, Finish* f) {
+int check_norm(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, const float* result, const void* ws,
+               size_t ws_bytes) {
   if (!g || !result) return set_error(GNS_ERR_INVALID, "null argument");
   if (n < 1) return set_error(GNS_ERR_INVALID, "need at least one tensor");
   if (norm_type != GNS_NORM_L2 && norm_type != GNS_NORM_INF) return set_error(GNS_ERR_INVALID, "unknown norm type");
@@ -1043,59 +1196,79 @@ int norm(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, f
   if (reinterpret_cast<uintptr_t>(ws) % 256) return set_error(GNS_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   if (ws_bytes < list_workspace(n))
     return set_error(GNS_ERR_WORKSPACE, "workspace too small: need " + std::to_string(list_workspace(n)) + " bytes");
-  const int inf = norm_type == GNS_NORM_INF;
-  *f = {static_cast<Slot*>(ws), call_number(), result, dev_status, 0, inf, max_norm, eps};
+  return GNS_OK;
+}
+
+int not_empty(const gns_tensor* g, int n) {
+  int k = 0;
+  for (int i = 0; i < n; ++i) k += !empty(g[i]);
+  return k;
+}
+
+// The launches of a norm of `left` tensors that are not empty; finish: the last of them writes
+// the result.
+int norm_launches(const gns_tensor* g, int n, int left, void* stream, bool finish, Finish* f) {
   const Roles a = {{g}, 1, n};
-  int left = 0;  // tensors that no launch has taken yet
-  for (int i = 0; i < n; ++i) left += !empty(g[i]);
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
     const int grid = grid_for(l.start[l.count], NORM_BLOCKS);
     Slot* at = f->slots + f->nslots;
     f->nslots += grid;
     left -= l.count;
-    return launch("grad norm", inf ? norm_kernel<true, L> : norm_kernel<false, L>, grid, stream, false, l, at, *f,
+    return launch("grad norm", f->inf ? norm_kernel<true, L> : norm_kernel<false, L>, grid, stream, ALONE, l, at, *f,
                   static_cast<int>(finish && !left));
   };
-  if (!left && finish) return launch("grad norm", no_norm_kernel, 1, stream, false, *f);
-  int rc = each_list<FlatList<1, NORM_FLAT>>(a, THREADS * NORM_VEC, go);
-  if (!rc) rc = each_list<RowList<1, NORM_ROWS>>(a, THREADS * NORM_VEC, go);
-  return rc;
+  const int rc = each_list<FlatList<1, NORM_FLAT>>(a, THREADS * NORM_VEC, go);
+  return rc ? rc : each_list<RowList<1, NORM_ROWS>>(a, THREADS * NORM_VEC, go);
 }
 
 int grad_norm(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, float* result, void* ws,
               size_t ws_bytes, int32_t* dev_status, void* stream) {
-  Finish f;
-  return norm(g, n, norm_type, max_norm, eps, result, ws, ws_bytes, dev_status, stream, true, &f);
+  if (int rc = check_norm(g, n, norm_type, max_norm, eps, result, ws, ws_bytes)) return rc;
+  const int inf = norm_type == GNS_NORM_INF, left = not_empty(g, n);
+  Finish f = {static_cast<Slot*>(ws), call_number(), result, dev_status, 0, inf, max_norm, eps};
+  if (!left) return launch("grad norm", no_norm_kernel, 1, stream, ALONE, f);
+  const int rc = short_lists<1>({{g}, 1, n}, left, [&](const auto& l) {
+    using L = std::decay_t<decltype(l)>;
+    return launch("grad norm", inf ? short_kernel<true, false, L> : short_kernel<false, false, L>,
+                  short_blocks(l.start[l.count]), stream, CLUSTER, l, f, 0);
+  });
+  return rc <= 0 ? rc : norm_launches(g, n, left, stream, true, &f);
 }
 
 int clip_grads(const gns_tensor* g, const gns_tensor* out, int n, int norm_type, float max_norm, float eps,
                float* result, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
-  if (!g) return set_error(GNS_ERR_INVALID, "null argument");
+  if (int rc = check_norm(g, n, norm_type, max_norm, eps, result, ws, ws_bytes)) return rc;
   int in_place = 1;
   for (int i = 0; out && i < n; ++i) {
-    if (int rc = check_tensor(g[i], "grads", i)) return rc;
     if (int rc = check_tensor(out[i], "outs", i)) return rc;
     if (!same_shape(g[i], out[i])) return fail(GNS_ERR_INVALID, "outs", i, "must have its gradient's shape");
     if (g[i].dtype != out[i].dtype) return fail(GNS_ERR_INVALID, "outs", i, "must have its gradient's dtype");
     if (empty(g[i])) continue;
     if (g[i].x.ptr != out[i].x.ptr)
       in_place = 0;
-    else if (g[i].x.rows > 1 && g[i].x.ld != out[i].x.ld || g[i].x.count > 1 && g[i].x.stride != out[i].x.stride)
+    else if ((g[i].x.rows > 1 && g[i].x.ld != out[i].x.ld) || (g[i].x.count > 1 && g[i].x.stride != out[i].x.stride))
       return fail(GNS_ERR_INVALID, "outs", i, "may alias its gradient only with the same layout");
   }
-  Finish f;
-  if (int rc = norm(g, n, norm_type, max_norm, eps, result, ws, ws_bytes, dev_status, stream, false, &f)) return rc;
-  if (!f.nslots) return launch("clip", no_norm_kernel, 1, stream, false, f);
+  const int inf = norm_type == GNS_NORM_INF, left = not_empty(g, n);
+  Finish f = {static_cast<Slot*>(ws), call_number(), result, dev_status, 0, inf, max_norm, eps};
+  if (!left) return launch("clip", no_norm_kernel, 1, stream, ALONE, f);
   const Roles a = {{g, out ? out : g}, 2, n};
+  int rc = short_lists<2>(a, left, [&](const auto& l) {
+    using L = std::decay_t<decltype(l)>;
+    return launch("clip", inf ? short_kernel<true, true, L> : short_kernel<false, true, L>,
+                  short_blocks(l.start[l.count]), stream, CLUSTER, l, f, in_place);
+  });
+  if (rc <= 0) return rc;
+  if ((rc = norm_launches(g, n, left, stream, false, &f))) return rc;
   int first = 1;  // the launch that writes the result
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
-    const int rc = launch("clip", clip_kernel<L>, grid_for(l.start[l.count], CLIP_BLOCKS), stream, true, l, f, first, in_place);
+    const int rc = launch("clip", clip_kernel<L>, grid_for(l.start[l.count], CLIP_BLOCKS), stream, BEHIND, l, f, first, in_place);
     first = 0;
     return rc;
   };
-  int rc = each_list<FlatList<2, CLIP_FLAT>>(a, THREADS * CLIP_VEC, go);
+  rc = each_list<FlatList<2, CLIP_FLAT>>(a, THREADS * CLIP_VEC, go);
   return rc ? rc : each_list<RowList<2, CLIP_ROWS>>(a, THREADS * CLIP_VEC, go);
 }
 
@@ -1146,7 +1319,7 @@ int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, co
   const Roles lists = {{W, G, M, V, master}, 5, n};
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
-    return launch("AdamW", adamw_kernel<L>, grid_for(l.start[l.count], 8), stream, false, l, a);
+    return launch("AdamW", adamw_kernel<L>, grid_for(l.start[l.count], 8), stream, ALONE, l, a);
   };
   int rc = each_list<FlatList<5, ADAMW_FLAT>>(lists, THREADS, go);
   return rc ? rc : each_list<RowList<5, ADAMW_ROWS>>(lists, THREADS, go);
