@@ -54,6 +54,9 @@ constexpr int MAX_GRID = 1216;  // blocks of one launch at most
 #ifndef NORM_BLOCKS
 #define NORM_BLOCKS 4
 #endif
+#ifndef ADAMW_BLOCKS
+#define ADAMW_BLOCKS 3
+#endif
 #ifndef CLIP_BLOCKS
 #define CLIP_BLOCKS 4
 #endif
@@ -86,8 +89,8 @@ struct RowList {
   static constexpr int kRoles = R, kCap = CAP;
   void* ptr[R][CAP];
   long long ld[R][CAP], stride[R][CAP];
-  int rows[CAP];   // of one matrix
   int nrows[CAP];  // of all matrices
+  int rows[CAP];   // of one matrix; 0: rows lie evenly from the first matrix to the last
   int cols[CAP];
   // 2^64 / d + 1 for the units of a row and the rows of a matrix (0: d is 1)
   unsigned long long by_row[CAP], by_matrix[CAP];
@@ -124,59 +127,6 @@ GNS_DEV void ld_v4(uint32_t* w, const void* p) {
 GNS_DEV void st_v4(void* p, const uint32_t* w) {
   asm volatile("st.global.v4.b32 [%4], {%0, %1, %2, %3};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "l"(p)
                : "memory");
-}
-
-// align: 2 = every unit starts on 8 elements' bytes, 1 = on 16 bytes, 0 = on an element.
-// Elements from `valid` on are neither read nor written, and read as zero.
-GNS_DEV void load_unit(Unit& u, const void* base, long long off, bool f32, int align, int valid) {
-  if (f32) {
-    const uint32_t* p = static_cast<const uint32_t*>(base) + off;
-    if (valid == 8 && align == 2) {
-      ld_v8(u.w, p);
-    } else if (valid == 8 && align == 1) {
-      ld_v4(u.w, p);
-      ld_v4(u.w + 4, p + 4);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u.w[e] = e < valid ? p[e] : 0u;
-    }
-  } else {
-    const unsigned short* p = static_cast<const unsigned short*>(base) + off;
-    if (valid == 8 && align) {
-      ld_v4(u.w, p);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = 2 * e < valid ? p[2 * e] : 0u, hi = 2 * e + 1 < valid ? p[2 * e + 1] : 0u;
-        u.w[e] = lo | (hi << 16);
-      }
-    }
-  }
-}
-
-GNS_DEV void store_unit(const Unit& u, void* base, long long off, bool f32, int align, int valid) {
-  if (f32) {
-    uint32_t* p = static_cast<uint32_t*>(base) + off;
-    if (valid == 8 && align == 2) {
-      st_v8(p, u.w);
-    } else if (valid == 8 && align == 1) {
-      st_v4(p, u.w);
-      st_v4(p + 4, u.w + 4);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < valid) p[e] = u.w[e];
-    }
-  } else {
-    unsigned short* p = static_cast<unsigned short*>(base) + off;
-    if (valid == 8 && align) {
-      st_v4(p, u.w);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < valid) p[e] = static_cast<unsigned short>(u.w[e / 2] >> (16 * (e & 1)));
-    }
-  }
 }
 
 GNS_DEV void unpack(float (&x)[8], const Unit& u, int dt) {
@@ -222,10 +172,10 @@ GNS_DEV void pack(Unit& u, const float (&x)[8], int dt) {
 // ---------------------------------------------------------------------------------------
 // walking a list
 
-// The tensor that holds a chunk: the last one that starts at or before it.
+// The tensor that holds a chunk: the last one that starts at or before it, `lo` or a later one.
 template <class L>
-GNS_DEV int find_tensor(const L& l, int chunk) {
-  int lo = 0, hi = l.count - 1;
+GNS_DEV int find_tensor(const L& l, int chunk, int lo = 0) {
+  int hi = l.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (l.start[mid] <= chunk)
@@ -236,57 +186,113 @@ GNS_DEV int find_tensor(const L& l, int chunk) {
   return lo;
 }
 
-// Where unit j of a chunk of tensor t lies in every role, for units of 2^LOG elements and `per`
-// units a chunk; returns how many of its elements exist (0: none).
+// The chunks of one group of threads: a run. It crosses few tensors, where a stride over the list
+// crosses many at each step.
+struct Run {
+  int begin, end;
+};
+template <class L>
+GNS_DEV Run run_of(const L& l, int group, int groups) {
+  const long long total = l.start[l.count];
+  return {static_cast<int>(total * group / groups), static_cast<int>(total * (group + 1) / groups)};
+}
+
+// A unit of 2^LOG elements in every role, as a vector of this many bytes' alignment (`align`, as in
+// the list; 0: element by element). valid: its elements that exist, from the first on (0: no unit).
+// over: the elements behind them can be read too.
+template <int R>
+struct Place {
+  long long off[R];
+  int valid, align;
+  bool over;
+};
+
+// A flat tensor has whole units from element `head` on; what lies before and behind them, fewer
+// than 2 units, follows as units of one element. Where no head puts every role on a vector the
+// units count from its first element, and the last may be short.
 template <int R, int CAP>
-GNS_DEV int locate(const FlatList<R, CAP>& l, int t, int chunk, int per, int log, int j, long long (&off)[R]) {
-  const long long o = l.head[t] + ((static_cast<long long>(chunk - l.start[t]) * per + j) << log);
+GNS_DEV Place<R> place(const FlatList<R, CAP>& l, int t, long long unit, int log) {
+  Place<R> p;
+  long long o = unit << log;
+  const long long n = l.n[t];
+  if (l.align[t]) {
+    const int head = l.head[t];
+    const long long whole = (n - head) >> log;
+    if (unit < whole) {
+      o += head;
+      p.valid = 1 << log;
+      p.align = l.align[t];
+    } else {
+      const long long e = unit - whole;  // of n - whole units' edge elements
+      o = e < head ? e : e + (whole << log);
+      p.valid = o < n;
+      p.align = 0;
+    }
+  } else {
+    p.valid = static_cast<int>(max(0ll, min(n - o, 1ll << log)));
+    p.align = 0;
+  }
+  p.over = false;
 #pragma unroll
-  for (int r = 0; r < R; ++r) off[r] = o;
-  const long long left = l.n[t] - o, most = 1 << log;
-  const int valid = static_cast<int>(max(0ll, min(left, most)));
-  return l.align[t] && valid < most ? 0 : valid;  // what is left of a unit is an edge
+  for (int r = 0; r < R; ++r) p.off[r] = o;
+  return p;
 }
 
 // x / d by a product with inv = 2^64 / d + 1 (0 for d = 1): exact for 32-bit x and d, as
-// x < 2^32 times inv's error, below 1, stays under 2^64 / d. Dividing costs the rows' kernels
-// more than everything else they do with a vector.
+// x < 2^32 times inv's error, below 1, stays under 2^64 / d. A division costs more than all else
+// that is done with a vector.
 GNS_DEV uint32_t quotient(uint32_t x, unsigned long long inv) {
   return inv ? static_cast<uint32_t>(__umul64hi(x, inv)) : x;
 }
 
+// A unit of a row list, and the one `step` units on.
+struct Cursor {
+  uint32_t per_row;    // units
+  uint32_t col;        // unit of its row
+  unsigned long long row;
+};
 template <int R, int CAP>
-GNS_DEV int locate(const RowList<R, CAP>& l, int t, int chunk, int per, int log, int j, long long (&off)[R]) {
-  const uint32_t cols = static_cast<uint32_t>(l.cols[t]), width = 1u << log;
-  const uint32_t per_row = (cols + width - 1u) >> log;
-  const unsigned long long u0 = static_cast<unsigned long long>(chunk - l.start[t]) * per;
-  // the chunk's first row; a tensor of 2^32 units or more has it by a division
-  const unsigned long long row0 = (u0 >> 32) == 0 ? quotient(static_cast<uint32_t>(u0), l.by_row[t]) : u0 / per_row;
-  const uint32_t x = static_cast<uint32_t>(u0 - row0 * per_row) + static_cast<uint32_t>(j);
-  const uint32_t q = quotient(x, l.by_row[t]);
-  const unsigned long long row = row0 + q;
-  if (row >= l.nrows[t]) return 0;
-  const uint32_t c = (x - q * per_row) << log;
-  const uint32_t b = quotient(static_cast<uint32_t>(row), l.by_matrix[t]);
-  const uint32_t i = static_cast<uint32_t>(row) - b * static_cast<uint32_t>(l.rows[t]);
-#pragma unroll
-  for (int r = 0; r < R; ++r) off[r] = b * l.stride[r][t] + i * l.ld[r][t] + c;
-  return static_cast<int>(min(width, cols - c));
+GNS_DEV Cursor cursor(const RowList<R, CAP>& l, int t, unsigned long long unit, int log) {
+  Cursor c;
+  c.per_row = (static_cast<uint32_t>(l.cols[t]) + (1u << log) - 1u) >> log;
+  // a tensor of 2^32 units or more needs the division
+  c.row = (unit >> 32) == 0 ? quotient(static_cast<uint32_t>(unit), l.by_row[t]) : unit / c.per_row;
+  c.col = static_cast<uint32_t>(unit - c.row * c.per_row);
+  return c;
+}
+template <int R, int CAP>
+GNS_DEV void advance(const RowList<R, CAP>& l, int t, Cursor& c, uint32_t step) {
+  const uint32_t q = step < c.per_row ? 0u : quotient(step, l.by_row[t]);
+  c.row += q;
+  c.col += step - q * c.per_row;
+  if (c.col >= c.per_row) {
+    c.col -= c.per_row;
+    ++c.row;
+  }
 }
 
-// The edges of a flat tensor that starts on a unit boundary only `head` elements in: the elements
-// before its first unit and after its last whole one. The first threads of its first chunk take
-// one each. Returns this thread's, or -1.
-template <class T, int R, int CAP>
-GNS_DEV long long edge(const FlatList<R, CAP>& l, int t, int chunk, int log) {
-  if (chunk != l.start[t] || !l.align[t]) return -1;
-  const int i = T::rank(), head = l.head[t];
-  const int tail = static_cast<int>((l.n[t] - head) & ((1 << log) - 1));
-  return i < head ? i : i < head + tail ? l.n[t] - tail + (i - head) : -1;
+template <int R, int CAP>
+GNS_DEV Place<R> place(const RowList<R, CAP>& l, int t, const Cursor& c, int log) {
+  Place<R> p;
+  const uint32_t nrows = static_cast<uint32_t>(l.nrows[t]), at = c.col << log;
+  p.valid = c.row < nrows ? static_cast<int>(min(1u << log, static_cast<uint32_t>(l.cols[t]) - at)) : 0;
+  p.align = l.align[t];
+  // on 16 bytes a row's pitch holds its last vector whole; behind the last row there may be nothing
+  p.over = c.row + 1 < nrows;
+  const uint32_t row = static_cast<uint32_t>(c.row);
+  if (l.rows[t]) {
+    const uint32_t b = quotient(row, l.by_matrix[t]), i = row - b * static_cast<uint32_t>(l.rows[t]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) p.off[r] = b * l.stride[r][t] + i * l.ld[r][t] + at;
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) p.off[r] = row * l.ld[r][t] + at;
+  }
+  return p;
 }
-template <class T, int R, int CAP>
-GNS_DEV long long edge(const RowList<R, CAP>&, int, int, int) {
-  return -1;
+template <int R, int CAP>
+GNS_DEV Place<R> place(const RowList<R, CAP>& l, int t, long long unit, int log) {
+  return place(l, t, cursor(l, t, static_cast<unsigned long long>(unit), log), log);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -328,38 +334,50 @@ struct Vec {
 
 GNS_DEV int vec_log(int dt) { return dt == GNS_F32 ? 2 : 3; }
 
-// `valid` elements from `off` on; the others read as zero. align != 0: a whole vector starts on
-// 16 bytes.
-GNS_DEV void load_vec(Vec& u, const void* base, long long off, int log, int align, int valid) {
-  if (valid == (1 << log) && align) {
-    ld_v4(u.w, static_cast<const char*>(base) + (off << (4 - log)));
-  } else if (log == 2) {
-    const uint32_t* p = static_cast<const uint32_t*>(base) + off;
+// The elements of one role of a unit; those that do not exist read as zero.
+template <int R>
+GNS_DEV void load_vec(Vec& u, const void* base, const Place<R>& p, int r, int log) {
+  const int valid = p.valid;
+  if (p.align && (valid == 1 << log || (p.over && valid))) {
+    ld_v4(u.w, static_cast<const char*>(base) + (p.off[r] << (4 - log)));
+    if (valid != 1 << log) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) u.w[e] = e < valid ? p[e] : 0u;
+      for (int e = 0; e < 4; ++e) {
+        if (log == 2)
+          u.w[e] = e < valid ? u.w[e] : 0u;
+        else
+          u.w[e] = 2 * e + 1 < valid ? u.w[e] : 2 * e < valid ? u.w[e] & 0xffffu : 0u;
+      }
+    }
+  } else if (log == 2) {
+    const uint32_t* q = static_cast<const uint32_t*>(base) + p.off[r];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u.w[e] = e < valid ? q[e] : 0u;
   } else {
-    const unsigned short* p = static_cast<const unsigned short*>(base) + off;
+    const unsigned short* q = static_cast<const unsigned short*>(base) + p.off[r];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = 2 * e < valid ? p[2 * e] : 0u, hi = 2 * e + 1 < valid ? p[2 * e + 1] : 0u;
+      const uint32_t lo = 2 * e < valid ? q[2 * e] : 0u, hi = 2 * e + 1 < valid ? q[2 * e + 1] : 0u;
       u.w[e] = lo | (hi << 16);
     }
   }
 }
 
-GNS_DEV void store_vec(const Vec& u, void* base, long long off, int log, int align, int valid) {
-  if (valid == (1 << log) && align) {
-    st_v4(static_cast<char*>(base) + (off << (4 - log)), u.w);
+template <int R>
+GNS_DEV void store_vec(const Vec& u, void* base, const Place<R>& p, int r, int log) {
+  const int valid = p.valid;
+  if (p.align && valid == 1 << log) {
+    st_v4(static_cast<char*>(base) + (p.off[r] << (4 - log)), u.w);
   } else if (log == 2) {
-    uint32_t* p = static_cast<uint32_t*>(base) + off;
+    uint32_t* q = static_cast<uint32_t*>(base) + p.off[r];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (e < valid) p[e] = u.w[e];
+      if (e < valid) q[e] = u.w[e];
   } else {
-    unsigned short* p = static_cast<unsigned short*>(base) + off;
+    unsigned short* q = static_cast<unsigned short*>(base) + p.off[r];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < valid) p[e] = static_cast<unsigned short>(u.w[e / 2] >> (16 * (e & 1)));
+      if (e < valid) q[e] = static_cast<unsigned short>(u.w[e / 2] >> (16 * (e & 1)));
   }
 }
 
@@ -376,66 +394,82 @@ GNS_DEV float2 halves(uint32_t w) {
 
 
 // Loads this thread's N vectors of a chunk (of a group of W threads, vector k * W + rank is its
-// k-th), those beyond the last whole one as zeros. Nearly every chunk is whole: its loads go out
-// with nothing to work out for each. The one role that counts here, the gradients, is aligned
-// unless it shares its head with an output that is not.
+// k-th); what does not exist reads as zero. Nearly every chunk is whole: its loads go out with
+// nothing to work out for each.
 template <class T, int N, int R, int CAP>
 GNS_DEV void load_chunk(const FlatList<R, CAP>& l, int t, int chunk, int log, Vec (&u)[N]) {
   constexpr int W = T::kThreads;
-  const long long o = l.head[t] + (static_cast<long long>(chunk - l.start[t]) * (W * N) << log);
-  if (R == 1 || l.align[t]) {
-    const long long left = (l.n[t] - o) >> log;
-    const char* p = static_cast<const char*>(l.ptr[0][t]) + (o << (4 - log)) + T::rank() * 16;
-    if (left >= W * N) {
+  const long long u0 = static_cast<long long>(chunk - l.start[t]) * (W * N);
+  if (R > 1 && !l.align[t]) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
-    } else {
-      const int n = static_cast<int>(left);
+    for (int k = 0; k < N; ++k) load_vec(u[k], l.ptr[0][t], place(l, t, u0 + k * W + T::rank(), log), 0, log);
+    return;
+  }
+  const char* p = static_cast<const char*>(l.ptr[0][t]) + ((l.head[t] + (u0 << log)) << (4 - log)) + T::rank() * 16;
+  const long long whole = ((l.n[t] - l.head[t]) >> log) - u0;
+  if (whole >= W * N) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        u[k] = {};
-        if (k * W + T::rank() < n) ld_v4(u[k].w, p + k * W * 16);
-      }
-    }
+    for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
   } else {
-    const int n = static_cast<int>(min(l.n[t] - o, static_cast<long long>(W * N << log)));
+    const int n = static_cast<int>(whole) - T::rank();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int at = (k * W + T::rank()) << log;
-      load_vec(u[k], l.ptr[0][t], o + at, log, 0, max(0, min(n - at, 1 << log)));
+      u[k] = {};
+      if (k * W < n) ld_v4(u[k].w, p + k * W * 16);
     }
   }
+}
+
+// The edge element of this thread in a chunk (a thread has one at most), of a flat tensor whose
+// whole units load_chunk takes by themselves; valid = 0: none.
+template <class T, int N, int R, int CAP>
+GNS_DEV Place<R> edge_place(const FlatList<R, CAP>& l, int t, int chunk, int log) {
+  constexpr int W = T::kThreads;
+  const long long u0 = static_cast<long long>(chunk - l.start[t]) * (W * N);
+  const long long whole = ((l.n[t] - l.head[t]) >> log) - u0;
+  Place<R> p;
+  p.valid = 0;
+  if (whole < W * N && l.align[t]) {
+    // units whole, whole + 1, ... of this chunk: the first of them that is this thread's turn
+    const int first = max(static_cast<int>(whole), 0);
+    const int unit = first + ((T::rank() - first) & (W - 1));
+    if (unit < W * N) p = place(l, t, u0 + unit, log);
+  }
+  return p;
+}
+template <class T, int N, int R, int CAP>
+GNS_DEV Place<R> edge_place(const RowList<R, CAP>&, int, int, int) {
+  Place<R> p;
+  p.valid = 0;
+  return p;
 }
 
 template <class T, int N, int R, int CAP>
 GNS_DEV void load_chunk(const RowList<R, CAP>& l, int t, int chunk, int log, Vec (&u)[N]) {
+  constexpr int W = T::kThreads;
+  Cursor c = cursor(l, t, static_cast<unsigned long long>(chunk - l.start[t]) * (W * N) + T::rank(), log);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    long long off[R];
-    const int valid = locate(l, t, chunk, T::kThreads * N, log, k * T::kThreads + T::rank(), off);
-    load_vec(u[k], l.ptr[0][t], off[0], log, l.align[t], valid);
+    load_vec(u[k], l.ptr[0][t], place(l, t, c, log), 0, log);
+    advance(l, t, c, W);
   }
 }
 
-// Calls f(vectors, type) for this thread's vectors, N of a chunk at a time. The groups of T
-// threads of the launch (this one is `group` of `groups`) have one run of the chunks each: a run
-// crosses few tensors, where a stride over the list crosses many at each step.
+// Calls f(vectors, type) for this thread's vectors of a group's run, N of a chunk at a time.
 template <class T, int N, class L, class F>
 GNS_DEV void for_vectors(const L& l, int group, int groups, F f) {
-  const int total = l.start[l.count];
-  int chunk = static_cast<int>(static_cast<long long>(total) * group / groups);
-  const int end = static_cast<int>(static_cast<long long>(total) * (group + 1) / groups);
-  if (chunk >= end) return;
-  int t = find_tensor(l, chunk);
-  for (; chunk < end; ++chunk) {
+  const Run run = run_of(l, group, groups);
+  if (run.begin >= run.end) return;
+  int t = find_tensor(l, run.begin);
+  for (int chunk = run.begin; chunk < run.end; ++chunk) {
     while (l.start[t + 1] <= chunk) ++t;
     const int dt = l.type[t] & 3, log = vec_log(dt);
-    Vec u[N], h[N] = {};
-    const long long e = edge<T>(l, t, chunk, log);
-    if (e >= 0) load_vec(h[0], l.ptr[0][t], e, log, 0, 1);
+    const auto p = edge_place<T, N>(l, t, chunk, log);
+    Vec u[N], h[1];
+    if (p.valid) load_vec(h[0], l.ptr[0][t], p, 0, log);
     load_chunk<T>(l, t, chunk, log, u);
     f(u, dt);
-    if (e >= 0) f(h, dt);
+    if (p.valid) f(h, dt);
   }
 }
 
@@ -467,7 +501,7 @@ GNS_DEV float squares(const Vec (&u)[N], float pre) {
 template <bool SCALED, class T, int N, class L>
 GNS_DEV float sum_squares(const L& l, int group, int groups, float pre, uint32_t* bits) {
   float s = 0.f, lost = 0.f;
-  for_vectors<T, N>(l, group, groups, [&](const Vec (&u)[N], int dt) {
+  for_vectors<T, N>(l, group, groups, [&](const auto& u, int dt) {
     const float q = dt == GNS_F32    ? squares<GNS_F32, SCALED>(u, pre)
                     : dt == GNS_BF16 ? squares<GNS_BF16, SCALED>(u, pre)
                                      : squares<GNS_F16, SCALED>(u, pre);
@@ -476,7 +510,7 @@ GNS_DEV float sum_squares(const L& l, int group, int groups, float pre, uint32_t
     s = t;
     if (!SCALED) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) *bits |= (u[k].w[0] | u[k].w[1]) | (u[k].w[2] | u[k].w[3]);
+      for (const Vec& v : u) *bits |= (v.w[0] | v.w[1]) | (v.w[2] | v.w[3]);
     }
   });
   return isfinite(s) ? s + lost : s;
@@ -500,12 +534,12 @@ template <bool INF, class T, int N, int BT, class L>
 GNS_DEV Share block_share(const L& l, int group, int groups) {
   if (INF) {
     uint32_t m = 0;  // magnitudes order as their bits do, with every NaN above infinity
-    for_vectors<T, N>(l, group, groups, [&](const Vec (&u)[N], int dt) {
+    for_vectors<T, N>(l, group, groups, [&](const auto& u, int dt) {
 #pragma unroll
-      for (int k = 0; k < N; ++k)
+      for (const Vec& v : u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t w = u[k].w[e];
+          const uint32_t w = v.w[e];
           if (dt == GNS_F32) {
             m = max(m, w & 0x7fffffffu);
           } else {
@@ -696,83 +730,87 @@ template <class T, int N, int CAP>
 GNS_DEV void clip_chunk(const FlatList<2, CAP>& l, int t, int chunk, int dt, float scale) {
   constexpr int W = T::kThreads;
   const int log = vec_log(dt);
-  const long long o = l.head[t] + (static_cast<long long>(chunk - l.start[t]) * (W * N) << log);
+  const long long u0 = static_cast<long long>(chunk - l.start[t]) * (W * N);
   Vec u[N];
-  if (l.align[t]) {
-    const long long left = (l.n[t] - o) >> log;
-    const long long at = (o << (4 - log)) + T::rank() * 16;
+  if (l.align[t] && ((l.n[t] - l.head[t]) >> log) - u0 >= W * N) {
+    const long long at = ((l.head[t] + (u0 << log)) << (4 - log)) + T::rank() * 16;
     const char* p = static_cast<const char*>(l.ptr[0][t]) + at;
     char* q = static_cast<char*>(l.ptr[1][t]) + at;
-    if (left >= W * N) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
+    for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        scale_vec(u[k], scale, dt);
-        st_v4(q + k * W * 16, u[k].w);
-      }
-    } else {
-      const int n = static_cast<int>(left) - T::rank();
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (k * W < n) ld_v4(u[k].w, p + k * W * 16);
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (k * W < n) {
-          scale_vec(u[k], scale, dt);
-          st_v4(q + k * W * 16, u[k].w);
-        }
+    for (int k = 0; k < N; ++k) {
+      scale_vec(u[k], scale, dt);
+      st_v4(q + k * W * 16, u[k].w);
     }
     return;
   }
-  // gradient and output can not both be on 16 bytes: neighbouring threads take neighbouring elements
-  const int n = static_cast<int>(min(l.n[t] - o, static_cast<long long>(W * N << log)));
-  for (int i = T::rank(); i < n; i += W) {
-    load_vec(u[0], l.ptr[0][t], o + i, log, 0, 1);
-    scale_vec(u[0], scale, dt);
-    store_vec(u[0], l.ptr[1][t], o + i, log, 0, 1);
+  if (l.align[t]) {
+    const Place<2> e = edge_place<T, N>(l, t, chunk, log);
+    Vec h;
+    if (e.valid) load_vec(h, l.ptr[0][t], e, 0, log);
+    load_chunk<T>(l, t, chunk, log, u);
+    char* q = static_cast<char*>(l.ptr[1][t]) + ((l.head[t] + (u0 << log)) << (4 - log)) + T::rank() * 16;
+    const int n = static_cast<int>(((l.n[t] - l.head[t]) >> log) - u0) - T::rank();
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (k * W < n) {
+        scale_vec(u[k], scale, dt);
+        st_v4(q + k * W * 16, u[k].w);
+      }
+    if (e.valid) {
+      scale_vec(h, scale, dt);
+      store_vec(h, l.ptr[1][t], e, 1, log);
+    }
+    return;
+  }
+  Place<2> p[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    p[k] = place(l, t, u0 + k * W + T::rank(), log);
+    load_vec(u[k], l.ptr[0][t], p[k], 0, log);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    scale_vec(u[k], scale, dt);
+    store_vec(u[k], l.ptr[1][t], p[k], 1, log);
   }
 }
 
 template <class T, int N, int CAP>
 GNS_DEV void clip_chunk(const RowList<2, CAP>& l, int t, int chunk, int dt, float scale) {
+  constexpr int W = T::kThreads;
   const int log = vec_log(dt);
   Vec u[N];
-  long long off[N][2];
-  int valid[N];
+  Place<2> p[N];
+  Cursor c = cursor(l, t, static_cast<unsigned long long>(chunk - l.start[t]) * (W * N) + T::rank(), log);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    valid[k] = locate(l, t, chunk, T::kThreads * N, log, k * T::kThreads + T::rank(), off[k]);
-    load_vec(u[k], l.ptr[0][t], off[k][0], log, l.align[t], valid[k]);
+    p[k] = place(l, t, c, log);
+    load_vec(u[k], l.ptr[0][t], p[k], 0, log);
+    advance(l, t, c, W);
   }
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     scale_vec(u[k], scale, dt);
-    store_vec(u[k], l.ptr[1][t], off[k][1], log, l.align[t], valid[k]);
+    store_vec(u[k], l.ptr[1][t], p[k], 1, log);
   }
 }
 
-// Scales chunk, chunk - step, ... down to `end`.
+// Scales the chunks of a group's run, from its last one to its first: these are what reading the
+// run for the norm left in L2.
 template <class T, int N, class L>
-GNS_DEV void clip_chunks(const L& l, int chunk, int end, int step, float scale) {
-  if (chunk < end) return;
-  int t = find_tensor(l, chunk);
-  for (; chunk >= end; chunk -= step) {
+GNS_DEV void clip_chunks(const L& l, int group, int groups, float scale) {
+  const Run run = run_of(l, group, groups);
+  if (run.begin >= run.end) return;
+  int t = find_tensor(l, run.end - 1);
+  for (int chunk = run.end - 1; chunk >= run.begin; --chunk) {
     while (l.start[t] > chunk) --t;
-    const int dt = l.type[t] & 3;
-    const long long e = edge<T>(l, t, chunk, vec_log(dt));
-    if (e >= 0) {
-      Vec h;
-      load_vec(h, l.ptr[0][t], e, vec_log(dt), 0, 1);
-      scale_vec(h, scale, dt);
-      store_vec(h, l.ptr[1][t], e, vec_log(dt), 0, 1);
-    }
-    clip_chunk<T, N>(l, t, chunk, dt, scale);
+    clip_chunk<T, N>(l, t, chunk, l.type[t] & 3, scale);
   }
 }
 
-// Every block forms the norm from the partial sums (a few KB, in L2), which saves a launch; the
-// chunks go backwards, as the list's end is what the pass for the norm left in L2.
+// Every block forms the norm from the slots (a few KB, in L2), which saves a launch.
 template <class L>
 __global__ void __launch_bounds__(THREADS, CLIP_BLOCKS) clip_kernel(const __grid_constant__ L l, Finish f, int first,
                                                                    int in_place) {
@@ -781,7 +819,7 @@ __global__ void __launch_bounds__(THREADS, CLIP_BLOCKS) clip_kernel(const __grid
   finish_norm<false>(f, &norm, &scale);
   if (first && blockIdx.x == 0) write_result(f, norm, scale);
   if (in_place && scale == 1.f) return;  // g * 1 is g
-  clip_chunks<Block, CLIP_VEC>(l, l.start[l.count] - 1 - static_cast<int>(blockIdx.x), 0, gridDim.x, scale);
+  clip_chunks<Block, CLIP_VEC>(l, blockIdx.x, gridDim.x, scale);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -817,9 +855,7 @@ __global__ void __launch_bounds__(SHORT_THREADS) short_kernel(const __grid_const
   if (blockIdx.x == 0) write_result(f, norm, scale);
   if constexpr (CLIP) {
     if (in_place && scale == 1.f) return;
-    const int total = l.start[l.count];  // the run of chunks that this warp has read
-    clip_chunks<Warp, SHORT_VEC>(l, static_cast<int>(static_cast<long long>(total) * (group + 1) / groups) - 1,
-                                 static_cast<int>(static_cast<long long>(total) * group / groups), 1, scale);
+    clip_chunks<Warp, SHORT_VEC>(l, group, groups, scale);
   }
 }
 
@@ -855,42 +891,74 @@ GNS_DEV void adamw_unit(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[
   }
 }
 
-template <class L>
-GNS_DEV void adamw_at(const L& l, int t, const long long (&off)[5], int align, int valid, const AdamwArgs& a,
-                      const AdamwStep& s, bool* bad) {
-  const int wt = l.type[t] & 3, gt = (l.type[t] >> 2) & 3;
-  const bool master = l.type[t] & 16;
-  Unit uw, ug, um, uv;
-  if (master)
-    load_unit(uw, l.ptr[4][t], off[4], true, align, valid);
-  else
-    load_unit(uw, l.ptr[0][t], off[0], wt == GNS_F32, align, valid);
-  load_unit(ug, l.ptr[1][t], off[1], gt == GNS_F32, align, valid);
-  load_unit(um, l.ptr[2][t], off[2], true, align, valid);
-  load_unit(uv, l.ptr[3][t], off[3], true, align, valid);
-  float w[8], g[8], m[8], v[8];
-  unpack(w, uw, master ? (int)GNS_F32 : wt);
-  unpack(g, ug, gt);
-  unpack(m, um, GNS_F32);
-  unpack(v, uv, GNS_F32);
-  adamw_unit(w, g, m, v, a, s, valid, bad);
-  pack(um, m, GNS_F32);
-  store_unit(um, l.ptr[2][t], off[2], true, align, valid);
-  pack(uv, v, GNS_F32);
-  store_unit(uv, l.ptr[3][t], off[3], true, align, valid);
-  if (master) {
-    pack(um, w, GNS_F32);
-    store_unit(um, l.ptr[4][t], off[4], true, align, valid);
+// The elements of one role of a unit; those that do not exist read as zero. align 2: the unit
+// starts on 8 elements' bytes, 1: on 16 bytes.
+GNS_DEV void load_unit(Unit& u, const void* base, const Place<5>& p, int r, bool f32) {
+  const int valid = p.valid;
+  const bool whole = p.align && (valid == 8 || (p.over && valid));
+  if (f32) {
+    const uint32_t* q = static_cast<const uint32_t*>(base) + p.off[r];
+    if (whole && p.align == 2) {
+      ld_v8(u.w, q);
+    } else if (whole) {
+      ld_v4(u.w, q);
+      if (valid > 4) ld_v4(u.w + 4, q + 4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u.w[e] = e < valid ? q[e] : 0u;
+    }
+    if (whole && valid != 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u.w[e] = e < valid ? u.w[e] : 0u;
+    }
+  } else {
+    const unsigned short* q = static_cast<const unsigned short*>(base) + p.off[r];
+    if (whole) {
+      ld_v4(u.w, q);
+      if (valid != 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u.w[e] = 2 * e + 1 < valid ? u.w[e] : 2 * e < valid ? u.w[e] & 0xffffu : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = 2 * e < valid ? q[2 * e] : 0u, hi = 2 * e + 1 < valid ? q[2 * e + 1] : 0u;
+        u.w[e] = lo | (hi << 16);
+      }
+    }
   }
-  pack(uw, w, wt);
-  store_unit(uw, l.ptr[0][t], off[0], wt == GNS_F32, align, valid);
+}
+
+GNS_DEV void store_unit(const Unit& u, void* base, const Place<5>& p, int r, bool f32) {
+  const int valid = p.valid;
+  if (f32) {
+    uint32_t* q = static_cast<uint32_t*>(base) + p.off[r];
+    if (valid == 8 && p.align == 2) {
+      st_v8(q, u.w);
+    } else if (valid == 8 && p.align) {
+      st_v4(q, u.w);
+      st_v4(q + 4, u.w + 4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < valid) q[e] = u.w[e];
+    }
+  } else {
+    unsigned short* q = static_cast<unsigned short*>(base) + p.off[r];
+    if (valid == 8 && p.align) {
+      st_v4(q, u.w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < valid) q[e] = static_cast<unsigned short>(u.w[e / 2] >> (16 * (e & 1)));
+    }
+  }
 }
 
 template <class L>
-__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ L l, const __grid_constant__ AdamwArgs a) {
+__global__ void __launch_bounds__(THREADS, ADAMW_BLOCKS) adamw_kernel(const __grid_constant__ L l,
+                                                                     const __grid_constant__ AdamwArgs a) {
   const int total = l.start[l.count];
-  int chunk = blockIdx.x;
-  if (chunk >= total) return;
   AdamwStep s;
   s.scale = a.grad_scale ? *a.grad_scale : 1.f;
   s.step_size = a.step_size;
@@ -901,18 +969,37 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
     s.rsqrt_bc2 = 1.f / sqrtf(-expm1f(n * a.log_beta2));
   }
   bool bad = false;
-  int t = find_tensor(l, chunk);
-  for (; chunk < total; chunk += gridDim.x) {
-    while (l.start[t + 1] <= chunk) ++t;
-    long long off[5];
-    const int valid = locate(l, t, chunk, THREADS, 3, threadIdx.x, off);
-    if (valid) adamw_at(l, t, off, l.align[t], valid, a, s, &bad);
-    const long long e = edge<Block>(l, t, chunk, 3);
-    if (e >= 0) {
-#pragma unroll
-      for (int r = 0; r < 5; ++r) off[r] = e;
-      adamw_at(l, t, off, 0, 1, a, s, &bad);
+  int t = 0;
+  for (int chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
+    if (l.start[t + 1] <= chunk) t = find_tensor(l, chunk, t + 1);
+    const Place<5> p = place(l, t, static_cast<long long>(chunk - l.start[t]) * THREADS + threadIdx.x, 3);
+    if (!p.valid) continue;
+    const int wt = l.type[t] & 3, gt = (l.type[t] >> 2) & 3;
+    const bool master = l.type[t] & 16;
+    Unit uw, ug, um, uv;
+    if (master)
+      load_unit(uw, l.ptr[4][t], p, 4, true);
+    else
+      load_unit(uw, l.ptr[0][t], p, 0, wt == GNS_F32);
+    load_unit(ug, l.ptr[1][t], p, 1, gt == GNS_F32);
+    load_unit(um, l.ptr[2][t], p, 2, true);
+    load_unit(uv, l.ptr[3][t], p, 3, true);
+    float w[8], g[8], m[8], v[8];
+    unpack(w, uw, master ? (int)GNS_F32 : wt);
+    unpack(g, ug, gt);
+    unpack(m, um, GNS_F32);
+    unpack(v, uv, GNS_F32);
+    adamw_unit(w, g, m, v, a, s, p.valid, &bad);
+    pack(um, m, GNS_F32);
+    store_unit(um, l.ptr[2][t], p, 2, true);
+    pack(uv, v, GNS_F32);
+    store_unit(uv, l.ptr[3][t], p, 3, true);
+    if (master) {
+      pack(um, w, GNS_F32);
+      store_unit(um, l.ptr[4][t], p, 4, true);
     }
+    pack(uw, w, wt);
+    store_unit(uw, l.ptr[0][t], p, 0, wt == GNS_F32);
   }
   if (bad) set_status(a.status, GNS_DEVST_NONFINITE);
 }
@@ -1020,8 +1107,8 @@ int64_t put(FlatList<R, CAP>* l, int k, const Roles& a, int i) {
   l->head[k] = static_cast<unsigned char>(head);
   l->align[k] = static_cast<unsigned char>(align);
   const int log = vectors && a.role[0][i].dtype == GNS_F32 ? 2 : 3;
-  // an aligned tensor's last elements, less than a unit, are an edge of its first chunk
-  return std::max<int64_t>(1, (n - head + (align ? 0 : (1 << log) - 1)) >> log);
+  const int64_t whole = (n - head) >> log;
+  return align ? whole + (n - (whole << log)) : (n + (1 << log) - 1) >> log;
 }
 
 uint64_t inverse(int64_t d) { return d > 1 ? ~uint64_t(0) / static_cast<uint64_t>(d) + 1 : 0; }
@@ -1029,8 +1116,8 @@ uint64_t inverse(int64_t d) { return d > 1 ? ~uint64_t(0) / static_cast<uint64_t
 template <int R, int CAP>
 int64_t put(RowList<R, CAP>* l, int k, const Roles& a, int i) {
   const gns_batch& x = a.role[0][i].x;
-  l->rows[k] = static_cast<int>(x.rows);
   l->nrows[k] = static_cast<int>(x.count * x.rows);
+  bool even = true;  // matrices follow one another at their rows' pitch
   l->cols[k] = static_cast<int>(x.cols);
   uint64_t bits16 = 0, bits32 = 0;  // low bits of every address and step in bytes, 16-bit and f32
   for (int r = 0; r < R; ++r) {
@@ -1039,6 +1126,8 @@ int64_t put(RowList<R, CAP>* l, int k, const Roles& a, int i) {
     const gns_tensor& t = a.role[r][i];
     if (t.x.rows > 1) l->ld[r][k] = t.x.ld;
     if (t.x.count > 1) l->stride[r][k] = t.x.stride;
+    even &= t.x.count == 1 || t.x.rows == 1 || t.x.stride == t.x.rows * t.x.ld;
+    if (t.x.rows == 1) l->ld[r][k] = l->stride[r][k];
     const int es = size_of(t.dtype);
     (es == 4 ? bits32 : bits16) |= reinterpret_cast<uintptr_t>(t.x.ptr) | static_cast<uint64_t>(l->ld[r][k] * es) |
                                    static_cast<uint64_t>(l->stride[r][k] * es);
@@ -1048,6 +1137,7 @@ int64_t put(RowList<R, CAP>* l, int k, const Roles& a, int i) {
   const int log = R < 5 && a.role[0][i].dtype == GNS_F32 ? 2 : 3;
   const int64_t per_row = (x.cols + (1 << log) - 1) >> log;
   l->by_row[k] = inverse(per_row);
+  l->rows[k] = even ? 0 : static_cast<int>(x.rows);
   l->by_matrix[k] = inverse(x.rows);
   return x.count * x.rows * per_row;
 }
@@ -1319,7 +1409,7 @@ int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, co
   const Roles lists = {{W, G, M, V, master}, 5, n};
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
-    return launch("AdamW", adamw_kernel<L>, grid_for(l.start[l.count], 8), stream, ALONE, l, a);
+    return launch("AdamW", adamw_kernel<L>, grid_for(l.start[l.count], ADAMW_BLOCKS), stream, ALONE, l, a);
   };
   int rc = each_list<FlatList<5, ADAMW_FLAT>>(lists, THREADS, go);
   return rc ? rc : each_list<RowList<5, ADAMW_ROWS>>(lists, THREADS, go);
