@@ -42,24 +42,14 @@ struct Warp {
   GNS_DEV static int rank() { return threadIdx.x & 31; }
 };
 constexpr int MAX_GRID = 1216;  // blocks of one launch at most
-#ifndef LDH
-#define LDH ""
-#endif
-#ifndef NORM_VEC
-#define NORM_VEC 8
-#endif
-#ifndef CLIP_VEC
-#define CLIP_VEC 4
-#endif
-#ifndef NORM_BLOCKS
-#define NORM_BLOCKS 4
-#endif
-#ifndef ADAMW_BLOCKS
-#define ADAMW_BLOCKS 3
-#endif
-#ifndef CLIP_BLOCKS
-#define CLIP_BLOCKS 4
-#endif
+// Vectors a thread takes at a time, and blocks on an SM. 4 blocks of 8 loads of 16 bytes a thread
+// (128 KB a SM in flight) read fastest: 8.6 GB at 7.3 TB/s, where 8 blocks of 4 read 7.1 and 5
+// blocks of 8 7.2; for clipping a GB of layers 3 blocks of 4 take 546 us, 4 of 4 560, 5 of 2 550, 3
+// of 8 562, and rows with a pitch 4 blocks of 4 (63 us; 3: 69, 5 of 2: 75).
+constexpr int NORM_VEC = 8, NORM_BLOCKS = 4, CLIP_VEC = 4, CLIP_BLOCKS = 3, CLIP_ROW_BLOCKS = 4;
+// AdamW: one unit a thread; 524 M weights take 3 blocks 2254 us, 4 take 2390, 2
+// 2690; rows with a pitch 3 in 157 us, 4 in 144.
+constexpr int ADAMW_BLOCKS = 3, ADAMW_ROW_BLOCKS = 4;
 
 // ---------------------------------------------------------------------------------------
 // lists as kernel parameters (at most 32,764 bytes of parameters a launch)
@@ -80,6 +70,10 @@ struct FlatList {
   unsigned char head[CAP];   // elements before the first unit
   int count;
 };
+
+// align of rows on 16 bytes whose pitch is their own length up to the next 16 bytes, from the first
+// matrix to the last, in every role.
+constexpr int TIGHT = 3;
 
 template <int R, int CAP>
 struct RowList {
@@ -108,7 +102,7 @@ struct Unit {
 };
 
 GNS_DEV void ld_v8(uint32_t (&w)[8], const void* p) {
-  asm volatile("ld.global" LDH ".v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                : "l"(p)
                : "memory");
@@ -119,7 +113,7 @@ GNS_DEV void st_v8(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 GNS_DEV void ld_v4(uint32_t* w, const void* p) {
-  asm volatile("ld.global" LDH ".v4.b32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                : "l"(p)
                : "memory");
@@ -172,10 +166,9 @@ GNS_DEV void pack(Unit& u, const float (&x)[8], int dt) {
 // ---------------------------------------------------------------------------------------
 // walking a list
 
-// The tensor that holds a chunk: the last one that starts at or before it, `lo` or a later one.
+// The tensor that holds a chunk, the last one that starts at or before it, of tensors lo .. hi.
 template <class L>
-GNS_DEV int find_tensor(const L& l, int chunk, int lo = 0) {
-  int hi = l.count - 1;
+GNS_DEV int find_tensor(const L& l, int chunk, int lo, int hi) {
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (l.start[mid] <= chunk)
@@ -334,21 +327,24 @@ struct Vec {
 
 GNS_DEV int vec_log(int dt) { return dt == GNS_F32 ? 2 : 3; }
 
+// Zeroes the elements from `valid` on.
+GNS_DEV void keep(Vec& u, int valid, int log) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (log == 2)
+      u.w[e] = e < valid ? u.w[e] : 0u;
+    else
+      u.w[e] = 2 * e + 1 < valid ? u.w[e] : 2 * e < valid ? u.w[e] & 0xffffu : 0u;
+  }
+}
+
 // The elements of one role of a unit; those that do not exist read as zero.
 template <int R>
 GNS_DEV void load_vec(Vec& u, const void* base, const Place<R>& p, int r, int log) {
   const int valid = p.valid;
   if (p.align && (valid == 1 << log || (p.over && valid))) {
     ld_v4(u.w, static_cast<const char*>(base) + (p.off[r] << (4 - log)));
-    if (valid != 1 << log) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (log == 2)
-          u.w[e] = e < valid ? u.w[e] : 0u;
-        else
-          u.w[e] = 2 * e + 1 < valid ? u.w[e] : 2 * e < valid ? u.w[e] & 0xffffu : 0u;
-      }
-    }
+    if (valid != 1 << log) keep(u, valid, log);
   } else if (log == 2) {
     const uint32_t* q = static_cast<const uint32_t*>(base) + p.off[r];
 #pragma unroll
@@ -444,10 +440,33 @@ GNS_DEV Place<R> edge_place(const RowList<R, CAP>&, int, int, int) {
   return p;
 }
 
+// Whether a chunk of W * N units from u0 on ends before the last unit of rows whose pitch is
+// their own length up to the next vector (as empty_padded makes them): its vectors then lie behind
+// one another, and only what each row's last one holds has to be looked at.
+template <int R, int CAP>
+GNS_DEV bool behind_one_another(const RowList<R, CAP>& l, int t, unsigned long long u0, int n, int log) {
+  const unsigned long long per_row = (static_cast<uint32_t>(l.cols[t]) + (1u << log) - 1u) >> log;
+  return l.align[t] == TIGHT && u0 + n < per_row * static_cast<uint32_t>(l.nrows[t]);
+}
+
 template <class T, int N, int R, int CAP>
 GNS_DEV void load_chunk(const RowList<R, CAP>& l, int t, int chunk, int log, Vec (&u)[N]) {
   constexpr int W = T::kThreads;
-  Cursor c = cursor(l, t, static_cast<unsigned long long>(chunk - l.start[t]) * (W * N) + T::rank(), log);
+  const unsigned long long u0 = static_cast<unsigned long long>(chunk - l.start[t]) * (W * N);
+  if (behind_one_another(l, t, u0, W * N, log)) {
+    const char* p = static_cast<const char*>(l.ptr[0][t]) + (u0 + T::rank()) * 16;
+#pragma unroll
+    for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
+    Cursor c = cursor(l, t, u0 + T::rank(), log);
+    const int last = l.cols[t] - static_cast<int>((c.per_row - 1) << log);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if (c.col == c.per_row - 1) keep(u[k], last, log);
+      advance(l, t, c, W);
+    }
+    return;
+  }
+  Cursor c = cursor(l, t, u0 + T::rank(), log);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     load_vec(u[k], l.ptr[0][t], place(l, t, c, log), 0, log);
@@ -460,7 +479,7 @@ template <class T, int N, class L, class F>
 GNS_DEV void for_vectors(const L& l, int group, int groups, F f) {
   const Run run = run_of(l, group, groups);
   if (run.begin >= run.end) return;
-  int t = find_tensor(l, run.begin);
+  int t = find_tensor(l, run.begin, 0, l.count - 1);
   for (int chunk = run.begin; chunk < run.end; ++chunk) {
     while (l.start[t + 1] <= chunk) ++t;
     const int dt = l.type[t] & 3, log = vec_log(dt);
@@ -781,9 +800,28 @@ template <class T, int N, int CAP>
 GNS_DEV void clip_chunk(const RowList<2, CAP>& l, int t, int chunk, int dt, float scale) {
   constexpr int W = T::kThreads;
   const int log = vec_log(dt);
+  const unsigned long long u0 = static_cast<unsigned long long>(chunk - l.start[t]) * (W * N);
   Vec u[N];
+  if (behind_one_another(l, t, u0, W * N, log)) {
+    const char* p = static_cast<const char*>(l.ptr[0][t]) + (u0 + T::rank()) * 16;
+    char* q = static_cast<char*>(l.ptr[1][t]) + (u0 + T::rank()) * 16;
+#pragma unroll
+    for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
+    Cursor c = cursor(l, t, u0 + T::rank(), log);
+    Place<2> e;
+    e.align = 1;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      scale_vec(u[k], scale, dt);
+      e.valid = c.col == c.per_row - 1 ? l.cols[t] - static_cast<int>(c.col << log) : 1 << log;
+      e.off[1] = 0;
+      store_vec(u[k], q + k * W * 16, e, 1, log);
+      advance(l, t, c, W);
+    }
+    return;
+  }
   Place<2> p[N];
-  Cursor c = cursor(l, t, static_cast<unsigned long long>(chunk - l.start[t]) * (W * N) + T::rank(), log);
+  Cursor c = cursor(l, t, u0 + T::rank(), log);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     p[k] = place(l, t, c, log);
@@ -803,7 +841,7 @@ template <class T, int N, class L>
 GNS_DEV void clip_chunks(const L& l, int group, int groups, float scale) {
   const Run run = run_of(l, group, groups);
   if (run.begin >= run.end) return;
-  int t = find_tensor(l, run.end - 1);
+  int t = find_tensor(l, run.end - 1, 0, l.count - 1);
   for (int chunk = run.end - 1; chunk >= run.begin; --chunk) {
     while (l.start[t] > chunk) --t;
     clip_chunk<T, N>(l, t, chunk, l.type[t] & 3, scale);
@@ -812,14 +850,18 @@ GNS_DEV void clip_chunks(const L& l, int group, int groups, float scale) {
 
 // Every block forms the norm from the slots (a few KB, in L2), which saves a launch.
 template <class L>
-__global__ void __launch_bounds__(THREADS, CLIP_BLOCKS) clip_kernel(const __grid_constant__ L l, Finish f, int first,
+__global__ void __launch_bounds__(THREADS, L::kRows ? CLIP_ROW_BLOCKS : CLIP_BLOCKS) clip_kernel(const __grid_constant__ L l, Finish f, int first,
                                                                    int in_place) {
   grid_dep_wait();
   float norm, scale;
   finish_norm<false>(f, &norm, &scale);
   if (first && blockIdx.x == 0) write_result(f, norm, scale);
   if (in_place && scale == 1.f) return;  // g * 1 is g
-  clip_chunks<Block, CLIP_VEC>(l, blockIdx.x, gridDim.x, scale);
+  int t = l.count - 1;
+  for (int chunk = l.start[l.count] - 1 - static_cast<int>(blockIdx.x); chunk >= 0; chunk -= gridDim.x) {
+    if (l.start[t] > chunk) t = find_tensor(l, chunk, 0, t - 1);
+    clip_chunk<Block, CLIP_VEC>(l, t, chunk, l.type[t] & 3, scale);
+  }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -956,7 +998,7 @@ GNS_DEV void store_unit(const Unit& u, void* base, const Place<5>& p, int r, boo
 }
 
 template <class L>
-__global__ void __launch_bounds__(THREADS, ADAMW_BLOCKS) adamw_kernel(const __grid_constant__ L l,
+__global__ void __launch_bounds__(THREADS, L::kRows ? ADAMW_ROW_BLOCKS : ADAMW_BLOCKS) adamw_kernel(const __grid_constant__ L l,
                                                                      const __grid_constant__ AdamwArgs a) {
   const int total = l.start[l.count];
   AdamwStep s;
@@ -971,7 +1013,7 @@ __global__ void __launch_bounds__(THREADS, ADAMW_BLOCKS) adamw_kernel(const __gr
   bool bad = false;
   int t = 0;
   for (int chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
-    if (l.start[t + 1] <= chunk) t = find_tensor(l, chunk, t + 1);
+    if (l.start[t + 1] <= chunk) t = find_tensor(l, chunk, t + 1, l.count - 1);
     const Place<5> p = place(l, t, static_cast<long long>(chunk - l.start[t]) * THREADS + threadIdx.x, 3);
     if (!p.valid) continue;
     const int wt = l.type[t] & 3, gt = (l.type[t] >> 2) & 3;
@@ -1138,6 +1180,9 @@ int64_t put(RowList<R, CAP>* l, int k, const Roles& a, int i) {
   const int64_t per_row = (x.cols + (1 << log) - 1) >> log;
   l->by_row[k] = inverse(per_row);
   l->rows[k] = even ? 0 : static_cast<int>(x.rows);
+  bool tight = R < 5 && even && on16;
+  for (int r = 0; r < R; ++r) tight &= l->ld[r][k] == per_row << log;
+  if (tight) l->align[k] = TIGHT;
   l->by_matrix[k] = inverse(x.rows);
   return x.count * x.rows * per_row;
 }
@@ -1166,10 +1211,7 @@ int fill(L* l, const Roles& a, int from, int64_t chunk_units) {
 }
 
 // Lists of one launch: how many tensors its parameters hold.
-#ifndef SMALL
-#define SMALL 64
-#endif
-constexpr int SMALL_LIST = SMALL;
+constexpr int SMALL_LIST = 64;
 constexpr int NORM_FLAT = 1024, NORM_ROWS = 448, CLIP_FLAT = 768, CLIP_ROWS = 320, ADAMW_FLAT = 512, ADAMW_ROWS = 176;
 
 static_assert(sizeof(FlatList<1, NORM_FLAT>) < 32000 && sizeof(RowList<1, NORM_ROWS>) < 32000, "kernel parameters");
@@ -1354,7 +1396,7 @@ int clip_grads(const gns_tensor* g, const gns_tensor* out, int n, int norm_type,
   int first = 1;  // the launch that writes the result
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
-    const int rc = launch("clip", clip_kernel<L>, grid_for(l.start[l.count], CLIP_BLOCKS), stream, BEHIND, l, f, first, in_place);
+    const int rc = launch("clip", clip_kernel<L>, grid_for(l.start[l.count], L::kRows ? CLIP_ROW_BLOCKS : CLIP_BLOCKS), stream, BEHIND, l, f, first, in_place);
     first = 0;
     return rc;
   };
@@ -1409,7 +1451,7 @@ int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, co
   const Roles lists = {{W, G, M, V, master}, 5, n};
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
-    return launch("AdamW", adamw_kernel<L>, grid_for(l.start[l.count], ADAMW_BLOCKS), stream, ALONE, l, a);
+    return launch("AdamW", adamw_kernel<L>, grid_for(l.start[l.count], L::kRows ? ADAMW_ROW_BLOCKS : ADAMW_BLOCKS), stream, ALONE, l, a);
   };
   int rc = each_list<FlatList<5, ADAMW_FLAT>>(lists, THREADS, go);
   return rc ? rc : each_list<RowList<5, ADAMW_ROWS>>(lists, THREADS, go);
