@@ -270,6 +270,13 @@ GNS_API int gns_muon_step(const gns_batch* W, const gns_batch* G, const gns_batc
                   int ngroups, const gns_muon_params* muon, const gns_ns_params* ns, void* ws,
                   size_t ws_bytes, int32_t* dev_status, void* stream);
 
+/* gns_muon_step with c G in place of G, c = *grad_scale (a device float, e.g. result + 1 of
+ * gns_grad_norm: the gradients are then clipped without a pass of their own); NULL: c = 1. The
+ * product c g is formed in fp32 and enters the fp32 sum of the momentum update unrounded. */
+GNS_API int gns_muon_step_scaled(const gns_batch* W, const gns_batch* G, const gns_batch* M, const gns_batch* V,
+                         int ngroups, const gns_muon_params* muon, const gns_ns_params* ns, const float* grad_scale,
+                         void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
 /* Selection step of Dion3 Algorithm 4 for one bf16 batch m: per matrix, the
  * k rows (columns when rows > cols) of largest exact l1 norm, ties to the lower index,
  * written ascending to idx[b*k .. b*k+k-1] (device int32). When gathered != NULL it also

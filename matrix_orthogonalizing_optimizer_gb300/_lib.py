@@ -36,7 +36,7 @@ EXPORTS = [
     "gns_gram_ns_batched", "gns_ns_standard_batched", "gns_sym_gemm_xxt", "gns_sym_gemm",
     "gns_sym_poly_update", "gns_muon_step", "gns_frac_row_select", "gns_profile_set", "gns_profile_query", "gns_gram_ns_batched_noalloc",
     "gns_selftest_bounded_wait",
-    "gns_list_workspace_size", "gns_grad_norm", "gns_clip_grads", "gns_adamw_step",
+    "gns_muon_step_scaled", "gns_list_workspace_size", "gns_grad_norm", "gns_clip_grads", "gns_adamw_step",
 ]
 
 
@@ -119,6 +119,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gns_sym_poly_update.argtypes = [B, B, B, B, B, f32, f32, f32, i32, i32, i32, vp, vp]
     lib.gns_muon_step.restype = i32
     lib.gns_muon_step.argtypes = [B, B, B, B, i32, P(GnsMuonParams), P(GnsNsParams), vp, sz, vp, vp]
+    lib.gns_muon_step_scaled.restype = i32
+    lib.gns_muon_step_scaled.argtypes = [B, B, B, B, i32, P(GnsMuonParams), P(GnsNsParams), vp, vp, sz, vp, vp]
     lib.gns_frac_row_select.restype = i32
     lib.gns_frac_row_select.argtypes = [B, i32, vp, B, vp, sz, vp]
     lib.gns_gram_ns_batched_noalloc.restype = i32

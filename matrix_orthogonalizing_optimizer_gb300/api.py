@@ -242,6 +242,14 @@ def check_status(status: Optional[torch.Tensor] = None, device=None, what: str =
     _report(what, status)
 
 
+def _device_scalar(name: str, t: Optional[torch.Tensor], dtype) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_cuda or t.numel() != 1:
+        raise ValueError(f"{name} must be a CUDA tensor of one {str(dtype)[6:]}")
+    return t.data_ptr()
+
+
 def _ns_common(fn_name: str, op: int, xs, outs, ns, workspace, status, stream, check_dev):
     xs = _as_list(xs)
     outs = [empty_padded(x.shape, x.dtype, x.device) for x in xs] if outs is None else _as_list(outs)
@@ -319,11 +327,13 @@ def sym_poly_update(R, Q, Z, RZ, q_scratch, a: float, b: float, c: float, q_is_i
 
 def muon_step(W, G, M, lr: Optional[float] = None, momentum: float = 0.95, weight_decay: float = 0.0, scale: float = 1.0,
               frac: float = 1.0, ns: Optional[NsParams] = None, workspace=None, status=None, stream=None,
-              V=None, params: Optional[MuonParams] = None, check: bool = True):
+              V=None, params: Optional[MuonParams] = None, check: bool = True,
+              grad_scale: Optional[torch.Tensor] = None):
     """One optimizer step in place on W and M (and V): Muon (frac = 1), the Dion3 fractional
     update (frac < 1), or the flavour named in `params` (which then supplies every
     hyper-parameter). V: NorMuon second moments, fp32 tensors (count, 1, min(rows, cols)) or
-    (1, min(rows, cols)) per group."""
+    (1, min(rows, cols)) per group. grad_scale: a CUDA float32 tensor of one element that
+    multiplies G on the way (the clip scale result[1:] of grad_norm); G itself stays as it is."""
     Ws, Gs, Ms = _as_list(W), _as_list(G), _as_list(M)
     ns = ns or NsParams()
     if params is None:
@@ -341,8 +351,9 @@ def muon_step(W, G, M, lr: Optional[float] = None, momentum: float = 0.95, weigh
     nsp = ns.c_struct()
     mp = params.c_struct()
     cs = _CallStatus(status, Ms[0].device, check, stream)
-    rc = load().gns_muon_step(wa, ga, ma, va, len(Ms), ctypes.byref(mp), ctypes.byref(nsp), ws.data_ptr(),
-                              ws.numel(), cs.ptr(), _stream_ptr(stream, Ms[0].device))
+    rc = load().gns_muon_step_scaled(wa, ga, ma, va, len(Ms), ctypes.byref(mp), ctypes.byref(nsp),
+                                     _device_scalar("grad_scale", grad_scale, torch.float32), ws.data_ptr(),
+                                     ws.numel(), cs.ptr(), _stream_ptr(stream, Ms[0].device))
     check_rc(rc, "gns_muon_step")
     cs.done("gns_muon_step")
 

@@ -120,15 +120,25 @@ constexpr int ROWS_PER_BLOCK = 4;
 // ---------------------------------------------------------------------------------------
 // momentum: M <- mu * M + G (mode 0; fp32 product, fp32 sum, one bf16 rounding) or
 // M <- M + G (mode 1), with the sum of squares of the stored new M in partials (when set).
+//
+// SCALED, here and in the kernels below that read G: c G in place of G, c = *gscale, the product
+// in fp32 and not rounded further before the sum.
 
 __device__ __forceinline__ float mom(float m, float g, float mu, int mode) {
   return mode == 0 ? __fadd_rn(__fmul_rn(mu, m), g) : __fadd_rn(m, g);
 }
 
+template <bool SCALED>
+__device__ __forceinline__ float scaled(float g, float c) {
+  return SCALED ? __fmul_rn(c, g) : g;
+}
+
+template <bool SCALED>
 __global__ void momentum_kernel(bf16* M, long long ldm, long long sm, const bf16* G, long long ldg, long long sg,
                                 int rows, int cols, float mu, int mode, int npart, float* partials, int* zero,
-                                int nzero) {
+                                int nzero, const float* gscale) {
   zero_and_release(zero, nzero);
+  const float gc = SCALED ? *gscale : 1.f;
   const int b = blockIdx.y, part = blockIdx.x;
   const int rp = (rows + npart - 1) / npart;
   const int r0 = part * rp, r1 = min(rows, r0 + rp);
@@ -146,7 +156,7 @@ __global__ void momentum_kernel(bf16* M, long long ldm, long long sm, const bf16
       const bf16* ge = reinterpret_cast<const bf16*>(&gv);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bf16 nv = f_to_bf16(mom(bf16_to_f(me[e]), bf16_to_f(ge[e]), mu, mode));
+        const bf16 nv = f_to_bf16(mom(bf16_to_f(me[e]), scaled<SCALED>(bf16_to_f(ge[e]), gc), mu, mode));
         me[e] = nv;
         const float f = bf16_to_f(nv);
         acc = fmaf(f, f, acc);
@@ -154,7 +164,7 @@ __global__ void momentum_kernel(bf16* M, long long ldm, long long sm, const bf16
       *reinterpret_cast<uint4*>(mr + c) = mv;
     }
     for (int c = cvec + threadIdx.x; c < cols; c += blockDim.x) {
-      const bf16 nv = f_to_bf16(mom(bf16_to_f(mr[c]), bf16_to_f(gr[c]), mu, mode));
+      const bf16 nv = f_to_bf16(mom(bf16_to_f(mr[c]), scaled<SCALED>(bf16_to_f(gr[c]), gc), mu, mode));
       mr[c] = nv;
       const float f = bf16_to_f(nv);
       acc = fmaf(f, f, acc);
@@ -326,11 +336,23 @@ __device__ __forceinline__ uint32_t bf16x2_add(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// M + c G of two bf16 pairs: each product and sum in fp32, the sum rounded once to bf16.
+template <bool SCALED>
+__device__ __forceinline__ uint32_t bf16x2_add_scaled(uint32_t a, uint32_t b, float c) {
+  if (!SCALED) return bf16x2_add(a, b);
+  const float lo = __fadd_rn(__uint_as_float(a << 16), __fmul_rn(c, __uint_as_float(b << 16)));
+  const float hi = __fadd_rn(__uint_as_float(a & 0xffff0000u), __fmul_rn(c, __uint_as_float(b & 0xffff0000u)));
+  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 // Rows of the (non-transposed) matrix: M <- M + G and the key of each row. One warp per
 // row; per-lane digits are summed across the warp (each sum < 2^37) and stored.
+template <bool SCALED>
 __global__ void frac_add_keys_rows_kernel(bf16* M, long long ldm, long long sm, const bf16* G, long long ldg,
                                           long long sg, int rows, int cols, int count, unsigned long long* keys,
-                                          int* nf) {
+                                          int* nf, const float* gscale) {
+  const float gc = SCALED ? *gscale : 1.f;
   const int warps_per_block = blockDim.x >> 5;
   const long long gw = (long long)blockIdx.x * warps_per_block + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -356,10 +378,10 @@ __global__ void frac_add_keys_rows_kernel(bf16* M, long long ldm, long long sm, 
       mn = *reinterpret_cast<const uint4*>(mr + cn);
       gn = *reinterpret_cast<const uint4*>(gr + cn);
     }
-    mv.x = bf16x2_add(mv.x, gv.x);
-    mv.y = bf16x2_add(mv.y, gv.y);
-    mv.z = bf16x2_add(mv.z, gv.z);
-    mv.w = bf16x2_add(mv.w, gv.w);
+    mv.x = bf16x2_add_scaled<SCALED>(mv.x, gv.x, gc);
+    mv.y = bf16x2_add_scaled<SCALED>(mv.y, gv.y, gc);
+    mv.z = bf16x2_add_scaled<SCALED>(mv.z, gv.z, gc);
+    mv.w = bf16x2_add_scaled<SCALED>(mv.w, gv.w, gc);
     *reinterpret_cast<uint4*>(mr + c) = mv;
     ka.add2(mv.x);
     ka.add2(mv.y);
@@ -369,7 +391,7 @@ __global__ void frac_add_keys_rows_kernel(bf16* M, long long ldm, long long sm, 
     gv = gn;
   }
   for (int c = cvec + lane; c < cols; c += 32) {
-    const bf16 nv = f_to_bf16(__fadd_rn(bf16_to_f(mr[c]), bf16_to_f(gr[c])));
+    const bf16 nv = f_to_bf16(__fadd_rn(bf16_to_f(mr[c]), scaled<SCALED>(bf16_to_f(gr[c]), gc)));
     mr[c] = nv;
     const uint32_t u = __bfloat16_as_ushort(nv);
     ka.add((u >> 7) & 0xFFu, u & 0x7Fu);
@@ -391,9 +413,11 @@ __global__ void frac_add_keys_rows_kernel(bf16* M, long long ldm, long long sm, 
 // Columns of the matrix (rows of its transpose): M <- M + G elementwise and the key of
 // every column, one thread per column over a chunk of rows, digits added with atomics.
 // keys / nf must be zero on entry.
+template <bool SCALED>
 __global__ void frac_add_keys_cols_kernel(bf16* M, long long ldm, long long sm, const bf16* G, long long ldg,
                                           long long sg, int rows, int cols, int rows_per_chunk,
-                                          unsigned long long* keys, int* nf) {
+                                          unsigned long long* keys, int* nf, const float* gscale) {
+  const float gc = SCALED ? *gscale : 1.f;
   const int b = blockIdx.z;
   const int c = blockIdx.x * blockDim.x + threadIdx.x;
   if (c >= cols) return;
@@ -403,7 +427,8 @@ __global__ void frac_add_keys_cols_kernel(bf16* M, long long ldm, long long sm, 
   KeyAcc ka;
   ka.init();
   for (int r = r0; r < r1; ++r) {
-    const bf16 nv = f_to_bf16(__fadd_rn(bf16_to_f(Mb[(long long)r * ldm + c]), bf16_to_f(Gb[(long long)r * ldg + c])));
+    const bf16 nv = f_to_bf16(__fadd_rn(bf16_to_f(Mb[(long long)r * ldm + c]),
+                                        scaled<SCALED>(bf16_to_f(Gb[(long long)r * ldg + c]), gc)));
     Mb[(long long)r * ldm + c] = nv;
     ka.add(__bfloat16_as_ushort(nv));
   }
@@ -468,10 +493,13 @@ struct ColKeys8 {
   }
 };
 
+template <bool SCALED>
 __global__ void __launch_bounds__(256) frac_add_keys_cols8_kernel(bf16* M, long long ldm, long long sm,
                                                                   const bf16* G, long long ldg, long long sg,
                                                                   int rows, int cols, int rows_per_chunk,
-                                                                  unsigned long long* keys, int* nf) {
+                                                                  unsigned long long* keys, int* nf,
+                                                                  const float* gscale) {
+  const float gc = SCALED ? *gscale : 1.f;
   const int b = blockIdx.z;
   const int c0 = (blockIdx.x * blockDim.x + threadIdx.x) * 8;
   if (c0 >= cols) return;
@@ -493,10 +521,10 @@ __global__ void __launch_bounds__(256) frac_add_keys_cols8_kernel(bf16* M, long 
       mn = *reinterpret_cast<const uint4*>(Mb + (long long)(r + 1) * ldm);
       gn = *reinterpret_cast<const uint4*>(Gb + (long long)(r + 1) * ldg);
     }
-    mv.x = bf16x2_add(mv.x, gv.x);
-    mv.y = bf16x2_add(mv.y, gv.y);
-    mv.z = bf16x2_add(mv.z, gv.z);
-    mv.w = bf16x2_add(mv.w, gv.w);
+    mv.x = bf16x2_add_scaled<SCALED>(mv.x, gv.x, gc);
+    mv.y = bf16x2_add_scaled<SCALED>(mv.y, gv.y, gc);
+    mv.z = bf16x2_add_scaled<SCALED>(mv.z, gv.z, gc);
+    mv.w = bf16x2_add_scaled<SCALED>(mv.w, gv.w, gc);
     *reinterpret_cast<uint4*>(Mb + (long long)r * ldm) = mv;
     const uint32_t w[4] = {mv.x, mv.y, mv.z, mv.w};
 #pragma unroll
@@ -1046,11 +1074,13 @@ __global__ void __launch_bounds__(256) normuon_rows_kernel(const float* s, float
 // One block of 256 threads per row; the row's new M stays in registers (VPT 16-byte
 // vectors per thread, cols = 2048 VPT at most, a multiple of 8): reads G, M, W and writes
 // M, W once, the algorithmic minimum of 10 bytes per element.
-template <int VPT>
+template <int VPT, bool SCALED>
 __global__ void __launch_bounds__(256) rownorm_fused_rows_kernel(bf16* M, long long ldm, long long sm, const bf16* G,
                                                                  long long ldg, long long sg, bf16* W, long long ldw,
                                                                  long long sw, int cols, float mu, float gamma,
-                                                                 float eps, float alpha, float beta) {
+                                                                 float eps, float alpha, float beta,
+                                                                 const float* gscale) {
+  const float gc = SCALED ? *gscale : 1.f;
   const int b = blockIdx.y, i = blockIdx.x;
   bf16* mr = M + (long long)b * sm + (long long)i * ldm;
   const bf16* gr = G + (long long)b * sg + (long long)i * ldg;
@@ -1067,7 +1097,7 @@ __global__ void __launch_bounds__(256) rownorm_fused_rows_kernel(bf16* M, long l
       const bf16* ge = reinterpret_cast<const bf16*>(&g4);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        me[q] = f_to_bf16(__fadd_rn(__fmul_rn(mu, bf16_to_f(me[q])), bf16_to_f(ge[q])));
+        me[q] = f_to_bf16(__fadd_rn(__fmul_rn(mu, bf16_to_f(me[q])), scaled<SCALED>(bf16_to_f(ge[q]), gc)));
         const float f = bf16_to_f(me[q]);
         acc = fmaf(f, f, acc);
       }
@@ -1259,11 +1289,12 @@ int launch_sumsq(gns_dtype dt, const MatRef& X, int64_t count, float* partials, 
 }
 
 int launch_momentum(const MatRef& M, const MatRef& G, int64_t count, float mu, int mode, float* partials,
-                    void* stream, std::string* err, int* zero, int nzero) {
+                    void* stream, std::string* err, int* zero, int nzero, const float* gscale) {
   dim3 grid(NPART, (unsigned)count);
-  momentum_kernel<<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride,
-                                               static_cast<const bf16*>(G.ptr), G.ld, G.stride, (int)M.rows,
-                                               (int)M.cols, mu, mode, NPART, partials, zero, nzero);
+  auto* kernel = gscale ? momentum_kernel<true> : momentum_kernel<false>;
+  kernel<<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride, static_cast<const bf16*>(G.ptr), G.ld,
+                                      G.stride, (int)M.rows, (int)M.cols, mu, mode, NPART, partials, zero, nzero,
+                                      gscale);
   return check_launch("momentum", err);
 }
 
@@ -1282,13 +1313,14 @@ int64_t gather_cols_blocks(int64_t k, int64_t rows) {
 }
 
 int launch_frac_add_keys(const MatRef& M, const MatRef& G, int64_t count, int trans, unsigned long long* keys,
-                         int* nf, void* stream, std::string* err) {
+                         int* nf, void* stream, std::string* err, const float* gscale) {
   if (!trans) {
     const long long rows_total = M.rows * count;
     const unsigned blocks = (unsigned)((rows_total + 7) / 8);
-    frac_add_keys_rows_kernel<<<blocks, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride,
+    auto* kernel = gscale ? frac_add_keys_rows_kernel<true> : frac_add_keys_rows_kernel<false>;
+    kernel<<<blocks, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride,
                                                              static_cast<const bf16*>(G.ptr), G.ld, G.stride,
-                                                             (int)M.rows, (int)M.cols, (int)count, keys, nf);
+                                                             (int)M.rows, (int)M.cols, (int)count, keys, nf, gscale);
   } else {
     cudaMemsetAsync(keys, 0, sizeof(unsigned long long) * KEY_DIGITS * M.cols * count, S(stream));
     cudaMemsetAsync(nf, 0, sizeof(int) * M.cols * count, S(stream));
@@ -1300,15 +1332,17 @@ int launch_frac_add_keys(const MatRef& M, const MatRef& G, int64_t count, int tr
       long long chunks = std::max(1LL, want / std::max(1LL, col_blocks * count));
       const int rpc = (int)std::max(64LL, (M.rows + chunks - 1) / chunks);
       dim3 grid((unsigned)col_blocks, (unsigned)((M.rows + rpc - 1) / rpc), (unsigned)count);
-      frac_add_keys_cols8_kernel<<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride,
+      auto* kernel = gscale ? frac_add_keys_cols8_kernel<true> : frac_add_keys_cols8_kernel<false>;
+      kernel<<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride,
                                                               static_cast<const bf16*>(G.ptr), G.ld, G.stride,
-                                                              (int)M.rows, (int)M.cols, rpc, keys, nf);
+                                                              (int)M.rows, (int)M.cols, rpc, keys, nf, gscale);
     } else {
       const int rpc = 256;
       dim3 grid((unsigned)((M.cols + 255) / 256), (unsigned)((M.rows + rpc - 1) / rpc), (unsigned)count);
-      frac_add_keys_cols_kernel<<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride,
+      auto* kernel = gscale ? frac_add_keys_cols_kernel<true> : frac_add_keys_cols_kernel<false>;
+      kernel<<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride,
                                                              static_cast<const bf16*>(G.ptr), G.ld, G.stride,
-                                                             (int)M.rows, (int)M.cols, rpc, keys, nf);
+                                                             (int)M.rows, (int)M.cols, rpc, keys, nf, gscale);
     }
   }
   return check_launch("frac_add_keys", err);
@@ -1442,20 +1476,21 @@ int launch_normuon_rows(const float* s, const MatRef& V, const int* idx, int64_t
 bool rownorm_fused_supported(int64_t cols) { return cols % 8 == 0 && cols <= 2048 * 8; }
 
 int launch_rownorm_fused_rows(const MatRef& M, const MatRef& G, const MatRef& W, int64_t count, float mu, float gamma,
-                              float eps, float alpha, float beta, void* stream, std::string* err) {
+                              float eps, float alpha, float beta, void* stream, std::string* err,
+                              const float* gscale) {
   dim3 grid((unsigned)M.rows, (unsigned)count);
   const int vpt = (int)((M.cols + 2047) / 2048);
 #define GNS_RN_ARGS                                                                                             \
   static_cast<bf16*>(M.ptr), M.ld, M.stride, static_cast<const bf16*>(G.ptr), G.ld, G.stride,                 \
-      static_cast<bf16*>(W.ptr), W.ld, W.stride, (int)M.cols, mu, gamma, eps, alpha, beta
+      static_cast<bf16*>(W.ptr), W.ld, W.stride, (int)M.cols, mu, gamma, eps, alpha, beta, gscale
   if (vpt <= 1)
-    rownorm_fused_rows_kernel<1><<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
+    (gscale ? rownorm_fused_rows_kernel<1, true> : rownorm_fused_rows_kernel<1, false>)<<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
   else if (vpt <= 2)
-    rownorm_fused_rows_kernel<2><<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
+    (gscale ? rownorm_fused_rows_kernel<2, true> : rownorm_fused_rows_kernel<2, false>)<<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
   else if (vpt <= 4)
-    rownorm_fused_rows_kernel<4><<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
+    (gscale ? rownorm_fused_rows_kernel<4, true> : rownorm_fused_rows_kernel<4, false>)<<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
   else
-    rownorm_fused_rows_kernel<8><<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
+    (gscale ? rownorm_fused_rows_kernel<8, true> : rownorm_fused_rows_kernel<8, false>)<<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
 #undef GNS_RN_ARGS
   return check_launch("rownorm_fused_rows", err);
 }

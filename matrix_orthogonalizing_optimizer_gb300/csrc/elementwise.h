@@ -17,8 +17,10 @@ constexpr int MAX_SELECT_N = 65536; // largest selection dimension (shared-memor
 // enqueued right after it, which then skips its own reset).
 int launch_sumsq(gns_dtype dt, const MatRef& X, int64_t count, float* partials, void* stream, std::string* err,
                  int* zero = nullptr, int nzero = 0);
+// gscale (optional, device): c G is added in place of G, c = *gscale; so for the other launchers that read G.
 int launch_momentum(const MatRef& M, const MatRef& G, int64_t count, float mu, int mode, float* partials,
-                    void* stream, std::string* err, int* zero = nullptr, int nzero = 0);
+                    void* stream, std::string* err, int* zero = nullptr, int nzero = 0,
+                    const float* gscale = nullptr);
 // npart: partials per matrix (NPART, or a gather's per-block sums, gather_cols_blocks).
 int launch_finalize_norm(const float* partials, int64_t count, float eps, float* inv, void* stream, std::string* err,
                          int64_t npart = NPART);
@@ -26,7 +28,7 @@ int launch_finalize_norm(const float* partials, int64_t count, float eps, float*
 // the per-block sums of squares it stores with bpart.
 int64_t gather_cols_blocks(int64_t k, int64_t rows);
 int launch_frac_add_keys(const MatRef& M, const MatRef& G, int64_t count, int trans, unsigned long long* keys,
-                         int* nf, void* stream, std::string* err);
+                         int* nf, void* stream, std::string* err, const float* gscale = nullptr);
 int launch_keys_only(const MatRef& M, int64_t count, int trans, unsigned long long* keys, int* nf, void* stream,
                      std::string* err);
 int launch_select_topk(unsigned long long* keys, const int* nf, int64_t n, int64_t k, int64_t count, int* idx,
@@ -64,7 +66,8 @@ int launch_normuon_rows(const float* s, const MatRef& V, const int* idx, int64_t
 // 16384): momentum, row norm and the scaled weight update in one kernel.
 bool rownorm_fused_supported(int64_t cols);
 int launch_rownorm_fused_rows(const MatRef& M, const MatRef& G, const MatRef& W, int64_t count, float mu, float gamma,
-                              float eps, float alpha, float beta, void* stream, std::string* err);
+                              float eps, float alpha, float beta, void* stream, std::string* err,
+                              const float* gscale = nullptr);
 // RowNorm scales r = gamma / max(sqrt(s), eps) over n entries.
 int launch_rownorm_scale(const float* s, int64_t n, float gamma, float eps, float* r, void* stream,
                          std::string* err);

@@ -1052,8 +1052,15 @@ int gns_sym_poly_update(const gns_batch* R, const gns_batch* Q, const gns_batch*
 int gns_muon_step(const gns_batch* W, const gns_batch* G, const gns_batch* M, const gns_batch* V, int ngroups,
                   const gns_muon_params* mp, const gns_ns_params* ns, void* ws, size_t ws_bytes,
                   int32_t* dev_status, void* stream) {
+  return gns_muon_step_scaled(W, G, M, V, ngroups, mp, ns, nullptr, ws, ws_bytes, dev_status, stream);
+}
+
+int gns_muon_step_scaled(const gns_batch* W, const gns_batch* G, const gns_batch* M, const gns_batch* V, int ngroups,
+                         const gns_muon_params* mp, const gns_ns_params* ns, const float* grad_scale, void* ws,
+                         size_t ws_bytes, int32_t* dev_status, void* stream) {
   if (!W || !G || !M || !mp) return fail(GNS_ERR_INVALID, "null argument");
   if (ngroups < 1) return fail(GNS_ERR_INVALID, "need at least one batch");
+  if (reinterpret_cast<uintptr_t>(grad_scale) % 4) return fail(GNS_ERR_INVALID, "grad_scale: unaligned");
   int rc;
   if ((rc = check_muon(*mp))) return rc;
   const bool normuon = step_flavor(*mp) == GNS_FLAVOR_NORMUON;
@@ -1098,11 +1105,11 @@ int gns_muon_step(const gns_batch* W, const gns_batch* G, const gns_batch* M, co
       // W <- (1 - lr wd) W - lr scale gamma R_eps(M) on the oriented rows of M
       if (!s.trans && rownorm_fused_supported(s.cols)) {
         if ((rc = launch_rownorm_fused_rows(mm, gm, wm, s.B, mu, mp->rownorm_gamma, mp->norm_eps, step_scale, decay,
-                                            stream, &err)))
+                                            stream, &err, grad_scale)))
           return fail(rc, err);
         continue;
       }
-      if ((rc = launch_momentum(mm, gm, s.B, mu, 0, nullptr, stream, &err))) return fail(rc, err);
+      if ((rc = launch_momentum(mm, gm, s.B, mu, 0, nullptr, stream, &err, nullptr, 0, grad_scale))) return fail(rc, err);
       if (!s.trans)
         rc = launch_row_sumsq(mm, s.rows, s.cols, s.B, mb.s, stream, &err);
       else
@@ -1146,7 +1153,7 @@ int gns_muon_step(const gns_batch* W, const gns_batch* G, const gns_batch* M, co
       const bool part_scale = !mb.use_std && mb.nsdt == GNS_BF16 && s.n >= kPartScaleMinN &&
                               !chain_ok(true, mb.nsdt, src, s.n, s.m, ns, fin);
       if ((rc = launch_momentum(mm, gm, s.B, mu, 0, partials, stream, &err, part_scale ? mb.gb.counters : nullptr,
-                                part_scale ? kMaxProgramOps * (int)s.B : 0)))
+                                part_scale ? kMaxProgramOps * (int)s.B : 0, grad_scale)))
         return fail(rc, err);
       if (!part_scale && (rc = launch_finalize_norm(partials, s.B, ns->eps, inv, stream, &err))) return fail(rc, err);
       if (mb.nsdt == GNS_F16) {
@@ -1204,7 +1211,7 @@ int gns_muon_step(const gns_batch* W, const gns_batch* G, const gns_batch* M, co
     // Dion3 Algorithm 4
     const int64_t k = mb.k;
     // M <- M + G, with the exact l1 keys of the oriented rows
-    if ((rc = launch_frac_add_keys(mm, gm, s.B, s.trans, mb.keys, mb.nf, stream, &err))) return fail(rc, err);
+    if ((rc = launch_frac_add_keys(mm, gm, s.B, s.trans, mb.keys, mb.nf, stream, &err, grad_scale))) return fail(rc, err);
     // selection
     if ((rc = launch_select_topk(mb.keys, mb.nf, s.n, k, s.B, mb.idx, stream, &err))) return fail(rc, err);
     // gather M[S, :] and its Frobenius norm; the error feedback (M[S] <- mu M[S]) rides

@@ -22,7 +22,7 @@ import torch
 from . import _lib
 from ._lib import GnsAdamwParams, GnsTensor, load
 from ._lib import check as check_rc
-from .api import _CallStatus, _dtype_code, alloc_workspace
+from .api import _CallStatus, _device_scalar, _dtype_code, alloc_workspace
 
 
 # Field by field a descriptor costs ten times what one packed write does.
@@ -222,14 +222,6 @@ class AdamWParams:
     def c_struct(self) -> GnsAdamwParams:
         return GnsAdamwParams(float(self.lr), float(self.beta1), float(self.beta2), float(self.eps),
                               float(self.weight_decay), int(self.step))
-
-
-def _device_scalar(name: str, t: Optional[torch.Tensor], dtype) -> Optional[int]:
-    if t is None:
-        return None
-    if t.dtype != dtype or not t.is_cuda or t.numel() != 1:
-        raise ValueError(f"{name} must be a CUDA tensor of one {str(dtype)[6:]}")
-    return t.data_ptr()
 
 
 def adamw_step(W, G, M, V, lr: Optional[float] = None, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
