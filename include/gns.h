@@ -289,7 +289,8 @@ GNS_API int gns_frac_row_select(const gns_batch* m, int k, int32_t* idx, const g
  *
  * A list is an array of n gns_tensor, n >= 1; bf16, fp16 and fp32 tensors may be mixed in it.
  * Tensors of one list may not overlap one another. A call makes one launch for about a
- * thousand (AdamW: five hundred) tensors, more launches for longer lists. */
+ * thousand (AdamW: five hundred) tensors without gaps, and one for some hundreds of rows with a
+ * pitch (ld > cols); longer lists take more. A workspace serves one call at a time. */
 
 /* Bytes of workspace of gns_grad_norm and gns_clip_grads for a list of n tensors (0 and the
  * last error when n < 1). */
@@ -300,7 +301,8 @@ GNS_API size_t gns_list_workspace_size(int n);
  *   result[1] = min(1, max_norm / (N + eps)); 1 when max_norm is infinity (no clipping)
  * result: two device floats. Sums are formed in a fixed order (the same bits for the same
  * list and sizes), squares never overflow or vanish: N is right over the whole range of the
- * types. A NaN gradient gives N = NaN and a NaN scale, an infinite one N = inf and scale 0;
+ * types. The call's last block gathers what the others have summed; should it have to wait for
+ * them beyond the library's limit, N is NaN and GNS_DEVST_TIMEOUT is set. A NaN gradient gives N = NaN and a NaN scale, an infinite one N = inf and scale 0;
  * either sets GNS_DEVST_NONFINITE. A list of empty tensors has N = 0. max_norm >= 0 and not
  * NaN, eps >= 0 and finite. */
 GNS_API int gns_grad_norm(const gns_tensor* grads, int n, int norm_type, float max_norm, float eps, float* result,

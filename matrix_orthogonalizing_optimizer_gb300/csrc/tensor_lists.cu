@@ -1,16 +1,16 @@
 // Operators over lists of tensors: the global norm of a list of gradients with the scale that
 // clips them (gns_grad_norm), the clipping itself (gns_clip_grads) and the AdamW step
-// (gns_adamw_step). All three stream every tensor once through the SMs and are bound by HBM
-// bandwidth on long lists and by launch latency on short ones.
+// (gns_adamw_step). They do 1 to 2 operations a byte, so HBM bounds them on long lists and the
+// launch on short ones; what their kernels are about is that the loads go out early and often
+// whatever the tensors' number, type, alignment and pitch.
 //
-// A launch carries the descriptors of many tensors in its parameters (no descriptor table in
-// device memory, so a call can be captured into a graph and needs no copy). The work is cut
-// into chunks of THREADS * UNITS units of 8 consecutive elements, no chunk crossing a tensor,
-// and block i takes chunks i, i + gridDim.x, ...
+// A launch carries the descriptors of many tensors in its parameters: there is no table in device
+// memory to write, so a call is kernels only and can be captured. Each tensor is cut into chunks;
+// blocks take chunks of the whole list and find the tensor of each in the parameters.
 //
-// Two layouts: a FlatList holds tensors whose elements lie without gaps in every role (a role
-// is one of the buffers an operator walks in step: gradients; weights, moments, master ...);
-// a RowList holds batches of rows with a pitch.
+// Two layouts: a FlatList holds tensors whose elements lie without gaps in every role (a role is
+// one of the buffers that an operator walks in step: gradients and outputs; weights, gradients,
+// moments, masters); a RowList holds batches of rows with a pitch. One launch has one layout.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -20,7 +20,7 @@
 #include <string>
 #include <type_traits>
 
-#include "gns.h"
+#include "../../include/gns.h"
 #include "common.cuh"
 #include "gemm.h"
 
@@ -41,21 +41,26 @@ struct Warp {
   static constexpr int kThreads = 32;
   GNS_DEV static int rank() { return threadIdx.x & 31; }
 };
+
 constexpr int MAX_GRID = 1216;  // blocks of one launch at most
-// Vectors a thread takes at a time, and blocks on an SM. 4 blocks of 8 loads of 16 bytes a thread
-// (128 KB a SM in flight) read fastest: 8.6 GB at 7.3 TB/s, where 8 blocks of 4 read 7.1 and 5
-// blocks of 8 7.2; for clipping a GB of layers 3 blocks of 4 take 546 us, 4 of 4 560, 5 of 2 550, 3
-// of 8 562, and rows with a pitch 4 blocks of 4 (63 us; 3: 69, 5 of 2: 75).
+
+// 16-byte vectors that a thread takes at a time, and blocks of a launch on an SM. Reading goes
+// fastest with 8 vectors and 4 blocks (128 KB an SM in flight: 8.6 GB at 7.3 TB/s; 4 vectors and 8
+// blocks 7.1, 8 and 5 7.2). Clipping 1.2 GB, which reads and writes: 4 vectors and 3 blocks 546 us,
+// 4 and 4 560, 2 and 5 550, 8 and 3 562; rows with a pitch 4 and 4 (63 us for 112 MB; 4 and 3 69, 2
+// and 5 75).
 constexpr int NORM_VEC = 8, NORM_BLOCKS = 4, CLIP_VEC = 4, CLIP_BLOCKS = 3, CLIP_ROW_BLOCKS = 4;
-// AdamW: one unit a thread; 524 M weights take 3 blocks 2254 us, 4 take 2390, 2
-// 2690; rows with a pitch 3 in 157 us, 4 in 144.
+// AdamW takes one unit of 8 elements a thread: 524 M bf16 weights with masters in 2.25 ms with 3
+// blocks, 2.39 with 4, 2.69 with 2; rows with a pitch 157 us with 3, 144 with 4.
 constexpr int ADAMW_BLOCKS = 3, ADAMW_ROW_BLOCKS = 4;
 
 // ---------------------------------------------------------------------------------------
 // lists as kernel parameters (at most 32,764 bytes of parameters a launch)
 
 // start[i]: the launch's first chunk of tensor i, start[count]: all chunks. type: the GNS_ types
-// of roles 0 and 1 in bits 0-1 and 2-3, bit 4 set when the tensor has every role.
+// of roles 0 and 1 in bits 0-1 and 2-3, bit 4 set when the tensor has a master (AdamW's role 4).
+// align: 2 = every unit starts on 8 elements' bytes in every role, 1 = on 16 bytes, 0 = on an
+// element.
 template <int R, int CAP>
 struct FlatList {
   template <int C>
@@ -66,14 +71,10 @@ struct FlatList {
   long long n[CAP];
   int start[CAP + 1];
   unsigned char type[CAP];
-  unsigned char align[CAP];  // what load_unit takes
-  unsigned char head[CAP];   // elements before the first unit
+  unsigned char align[CAP];
+  unsigned char head[CAP];  // elements before the first unit
   int count;
 };
-
-// align of rows on 16 bytes whose pitch is their own length up to the next 16 bytes, from the first
-// matrix to the last, in every role.
-constexpr int TIGHT = 3;
 
 template <int R, int CAP>
 struct RowList {
@@ -91,6 +92,9 @@ struct RowList {
   int start[CAP + 1];
   unsigned char type[CAP];
   unsigned char align[CAP];
+  // rows on 16 bytes whose pitch is their own length up to the next unit, from the first matrix to
+  // the last, in every role (as empty_padded makes them): units lie behind one another
+  unsigned char tight[CAP];
   int count;
 };
 
@@ -179,20 +183,10 @@ GNS_DEV int find_tensor(const L& l, int chunk, int lo, int hi) {
   return lo;
 }
 
-// The chunks of one group of threads: a run. It crosses few tensors, where a stride over the list
-// crosses many at each step.
-struct Run {
-  int begin, end;
-};
-template <class L>
-GNS_DEV Run run_of(const L& l, int group, int groups) {
-  const long long total = l.start[l.count];
-  return {static_cast<int>(total * group / groups), static_cast<int>(total * (group + 1) / groups)};
-}
-
-// A unit of 2^LOG elements in every role, as a vector of this many bytes' alignment (`align`, as in
-// the list; 0: element by element). valid: its elements that exist, from the first on (0: no unit).
-// over: the elements behind them can be read too.
+// A unit of 2^log elements in every role: one vector of the norm and of clipping (log 2 or 3), 8
+// elements of AdamW. off: its first element. valid: how many of its elements exist, from the first
+// on (0: no unit). align: as in the list. over: what lies behind the valid elements up to the end
+// of a vector can be read too.
 template <int R>
 struct Place {
   long long off[R];
@@ -387,8 +381,6 @@ GNS_DEV float2 halves(uint32_t w) {
 // ---------------------------------------------------------------------------------------
 // norm: sqrt(sum x^2) over the whole list, or max |x|
 
-
-
 // Loads this thread's N vectors of a chunk (of a group of W threads, vector k * W + rank is its
 // k-th); what does not exist reads as zero. Nearly every chunk is whole: its loads go out with
 // nothing to work out for each.
@@ -440,13 +432,12 @@ GNS_DEV Place<R> edge_place(const RowList<R, CAP>&, int, int, int) {
   return p;
 }
 
-// Whether a chunk of W * N units from u0 on ends before the last unit of rows whose pitch is
-// their own length up to the next vector (as empty_padded makes them): its vectors then lie behind
-// one another, and only what each row's last one holds has to be looked at.
+// Whether a chunk of n units from u0 on has only whole vectors to read: it ends before the last
+// unit of tight rows, so that only what each row's last vector holds has to be looked at.
 template <int R, int CAP>
 GNS_DEV bool behind_one_another(const RowList<R, CAP>& l, int t, unsigned long long u0, int n, int log) {
   const unsigned long long per_row = (static_cast<uint32_t>(l.cols[t]) + (1u << log) - 1u) >> log;
-  return l.align[t] == TIGHT && u0 + n < per_row * static_cast<uint32_t>(l.nrows[t]);
+  return l.tight[t] && u0 + n < per_row * static_cast<uint32_t>(l.nrows[t]);
 }
 
 template <class T, int N, int R, int CAP>
@@ -474,19 +465,21 @@ GNS_DEV void load_chunk(const RowList<R, CAP>& l, int t, int chunk, int log, Vec
   }
 }
 
-// Calls f(vectors, type) for this thread's vectors of a group's run, N of a chunk at a time.
-template <class T, int N, class L, class F>
-GNS_DEV void for_vectors(const L& l, int group, int groups, F f) {
-  const Run run = run_of(l, group, groups);
-  if (run.begin >= run.end) return;
-  int t = find_tensor(l, run.begin, 0, l.count - 1);
-  for (int chunk = run.begin; chunk < run.end; ++chunk) {
+// Calls f(vectors, type) for this thread's vectors of the block's run of chunks: a run crosses few
+// tensors, where a stride over the list crosses many at each step.
+template <class L, class F>
+GNS_DEV void for_vectors(const L& l, F f) {
+  const long long total = l.start[l.count];
+  const int begin = static_cast<int>(total * blockIdx.x / gridDim.x), end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+  if (begin >= end) return;
+  int t = find_tensor(l, begin, 0, l.count - 1);
+  for (int chunk = begin; chunk < end; ++chunk) {
     while (l.start[t + 1] <= chunk) ++t;
     const int dt = l.type[t] & 3, log = vec_log(dt);
-    const auto p = edge_place<T, N>(l, t, chunk, log);
-    Vec u[N], h[1];
+    const auto p = edge_place<Block, NORM_VEC>(l, t, chunk, log);
+    Vec u[NORM_VEC], h[1];
     if (p.valid) load_vec(h[0], l.ptr[0][t], p, 0, log);
-    load_chunk<T>(l, t, chunk, log, u);
+    load_chunk<Block>(l, t, chunk, log, u);
     f(u, dt);
     if (p.valid) f(h, dt);
   }
@@ -513,24 +506,32 @@ GNS_DEV float squares(const Vec (&u)[N], float pre) {
     }
   return q[0] + q[1];
 }
+template <bool SCALED, int N>
+GNS_DEV float squares(const Vec (&u)[N], float pre, int dt) {
+  return dt == GNS_F32    ? squares<GNS_F32, SCALED>(u, pre)
+         : dt == GNS_BF16 ? squares<GNS_BF16, SCALED>(u, pre)
+                          : squares<GNS_F16, SCALED>(u, pre);
+}
+template <int N>
+GNS_DEV uint32_t bits_of(const Vec (&u)[N]) {
+  uint32_t b = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) b |= (u[k].w[0] | u[k].w[1]) | (u[k].w[2] | u[k].w[3]);
+  return b;
+}
 
 // Sum of this thread's squares: up to 64 of a chunk in f32, these sums with the rounding error of
 // each addition kept beside them (Knuth's two-sum), as f32 holds too little for a long list and
 // f64, at 2 operations a clock and SM, took longer than the loads.
-template <bool SCALED, class T, int N, class L>
-GNS_DEV float sum_squares(const L& l, int group, int groups, float pre, uint32_t* bits) {
+template <bool SCALED, class L>
+GNS_DEV float sum_squares(const L& l, float pre, uint32_t* bits) {
   float s = 0.f, lost = 0.f;
-  for_vectors<T, N>(l, group, groups, [&](const auto& u, int dt) {
-    const float q = dt == GNS_F32    ? squares<GNS_F32, SCALED>(u, pre)
-                    : dt == GNS_BF16 ? squares<GNS_BF16, SCALED>(u, pre)
-                                     : squares<GNS_F16, SCALED>(u, pre);
+  for_vectors(l, [&](const auto& u, int dt) {
+    const float q = squares<SCALED>(u, pre, dt);
     const float t = __fadd_rn(s, q), b = __fsub_rn(t, s);
     lost += __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(q, b));
     s = t;
-    if (!SCALED) {
-#pragma unroll
-      for (const Vec& v : u) *bits |= (v.w[0] | v.w[1]) | (v.w[2] | v.w[3]);
-    }
+    if (!SCALED) *bits |= bits_of(u);
   });
   return isfinite(s) ? s + lost : s;
 }
@@ -541,39 +542,40 @@ struct Share {
   int e;
 };
 
-// This block's share of the norm, in every thread: its sum of squares or (INF) its largest
-// magnitude.
+// The largest magnitude of some vectors: magnitudes order as their bits do, with every NaN above
+// infinity.
+template <int N>
+GNS_DEV uint32_t largest(const Vec (&u)[N], int dt) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t w = u[k].w[e];
+      if (dt == GNS_F32) {
+        m = max(m, w & 0x7fffffffu);
+      } else {
+        const float2 x = dt == GNS_BF16 ? halves<GNS_BF16>(w) : halves<GNS_F16>(w);
+        m = max(m, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
+      }
+    }
+  return m;
+}
+
+// A block's share of the norm, in every thread: its sum of squares sum(pre), of the values scaled
+// by pre, bits being some of theirs that are set if any is.
 //
 // Squares of f32 and bf16 values leave f32's range long before the values do (above 2^64, below
 // 2^-63). A block whose sum says that this may have happened (it is above 2^100 or not finite, or
 // below 2^-80 though some bit is set) sums once more with the values scaled by 2^-100 or 2^100,
 // which is exact for every value that counts: the largest magnitudes become at most 2^28, and
 // where the sum lies below 2^-80 none is above 2^-40, so they become at most 2^60.
-template <bool INF, class T, int N, int BT, class L>
-GNS_DEV Share block_share(const L& l, int group, int groups) {
-  if (INF) {
-    uint32_t m = 0;  // magnitudes order as their bits do, with every NaN above infinity
-    for_vectors<T, N>(l, group, groups, [&](const auto& u, int dt) {
-#pragma unroll
-      for (const Vec& v : u)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t w = v.w[e];
-          if (dt == GNS_F32) {
-            m = max(m, w & 0x7fffffffu);
-          } else {
-            const float2 x = dt == GNS_BF16 ? halves<GNS_BF16>(w) : halves<GNS_F16>(w);
-            m = max(m, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
-          }
-        }
-    });
-    return {__uint_as_float(block_max<BT>(m)), 0};
-  }
-  uint32_t bits = 0;
-  const float s = block_sum<BT>(sum_squares<false, T, N>(l, group, groups, 1.f, &bits));
+template <int BT, class F>
+GNS_DEV Share square_share(F sum, const uint32_t& bits) {
+  const float s = block_sum<BT>(sum(1.f, std::false_type()));
   const int any = __syncthreads_or(bits != 0);
-  if (!(s <= 0x1p100f)) return {block_sum<BT>(sum_squares<true, T, N>(l, group, groups, 0x1p-100f, &bits)), 200};
-  if (s < 0x1p-80f && any) return {block_sum<BT>(sum_squares<true, T, N>(l, group, groups, 0x1p100f, &bits)), -200};
+  if (!(s <= 0x1p100f)) return {block_sum<BT>(sum(0x1p-100f, std::true_type())), 200};
+  if (s < 0x1p-80f && any) return {block_sum<BT>(sum(0x1p100f, std::true_type())), -200};
   return {s, 0};
 }
 
@@ -695,7 +697,15 @@ template <bool INF, class L>
 __global__ void __launch_bounds__(THREADS, NORM_BLOCKS) norm_kernel(const __grid_constant__ L l, Slot* slots, Finish f,
                                                                    int finish) {
   grid_dep_launch();
-  const Share s = block_share<INF, Block, NORM_VEC, THREADS>(l, blockIdx.x, gridDim.x);
+  Share s;
+  if (INF) {
+    uint32_t m = 0;
+    for_vectors(l, [&](const auto& u, int dt) { m = max(m, largest(u, dt)); });
+    s = {__uint_as_float(block_max<THREADS>(m)), 0};
+  } else {
+    uint32_t bits = 0;
+    s = square_share<THREADS>([&](float pre, auto scaled) { return sum_squares<scaled.value>(l, pre, &bits); }, bits);
+  }
   if (threadIdx.x == 0) put_slot(slots + blockIdx.x, s, f.call);
   if (finish && blockIdx.x == gridDim.x - 1) {
     float norm, scale;
@@ -713,8 +723,6 @@ __global__ void __launch_bounds__(THREADS) no_norm_kernel(Finish f) {
 
 // ---------------------------------------------------------------------------------------
 // clipping: out = round(scale * g); roles: gradient, output (the same pointers in place)
-
-
 
 template <int DT>
 GNS_DEV void scale_vec(Vec& u, float scale) {
@@ -744,114 +752,60 @@ GNS_DEV void scale_vec(Vec& u, float scale, int dt) {
     scale_vec<GNS_F16>(u, scale);
 }
 
-// Scales one chunk of tensor t, N vectors a thread of the group.
+// Stores this thread's N vectors of a chunk that load_chunk has loaded, into role 1.
 template <class T, int N, int CAP>
-GNS_DEV void clip_chunk(const FlatList<2, CAP>& l, int t, int chunk, int dt, float scale) {
+GNS_DEV void store_chunk(const FlatList<2, CAP>& l, int t, int chunk, int log, const Vec (&u)[N]) {
   constexpr int W = T::kThreads;
-  const int log = vec_log(dt);
   const long long u0 = static_cast<long long>(chunk - l.start[t]) * (W * N);
-  Vec u[N];
-  if (l.align[t] && ((l.n[t] - l.head[t]) >> log) - u0 >= W * N) {
-    const long long at = ((l.head[t] + (u0 << log)) << (4 - log)) + T::rank() * 16;
-    const char* p = static_cast<const char*>(l.ptr[0][t]) + at;
-    char* q = static_cast<char*>(l.ptr[1][t]) + at;
+  if (!l.align[t]) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      scale_vec(u[k], scale, dt);
-      st_v4(q + k * W * 16, u[k].w);
-    }
+    for (int k = 0; k < N; ++k) store_vec(u[k], l.ptr[1][t], place(l, t, u0 + k * W + T::rank(), log), 1, log);
     return;
   }
-  if (l.align[t]) {
-    const Place<2> e = edge_place<T, N>(l, t, chunk, log);
-    Vec h;
-    if (e.valid) load_vec(h, l.ptr[0][t], e, 0, log);
-    load_chunk<T>(l, t, chunk, log, u);
-    char* q = static_cast<char*>(l.ptr[1][t]) + ((l.head[t] + (u0 << log)) << (4 - log)) + T::rank() * 16;
-    const int n = static_cast<int>(((l.n[t] - l.head[t]) >> log) - u0) - T::rank();
+  char* q = static_cast<char*>(l.ptr[1][t]) + ((l.head[t] + (u0 << log)) << (4 - log)) + T::rank() * 16;
+  const long long whole = ((l.n[t] - l.head[t]) >> log) - u0;
+  if (whole >= W * N) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) st_v4(q + k * W * 16, u[k].w);
+  } else {
+    const int n = static_cast<int>(whole) - T::rank();
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      if (k * W < n) {
-        scale_vec(u[k], scale, dt);
-        st_v4(q + k * W * 16, u[k].w);
-      }
-    if (e.valid) {
-      scale_vec(h, scale, dt);
-      store_vec(h, l.ptr[1][t], e, 1, log);
-    }
-    return;
-  }
-  Place<2> p[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    p[k] = place(l, t, u0 + k * W + T::rank(), log);
-    load_vec(u[k], l.ptr[0][t], p[k], 0, log);
-  }
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    scale_vec(u[k], scale, dt);
-    store_vec(u[k], l.ptr[1][t], p[k], 1, log);
+      if (k * W < n) st_v4(q + k * W * 16, u[k].w);
   }
 }
 
 template <class T, int N, int CAP>
-GNS_DEV void clip_chunk(const RowList<2, CAP>& l, int t, int chunk, int dt, float scale) {
+GNS_DEV void store_chunk(const RowList<2, CAP>& l, int t, int chunk, int log, const Vec (&u)[N]) {
   constexpr int W = T::kThreads;
-  const int log = vec_log(dt);
   const unsigned long long u0 = static_cast<unsigned long long>(chunk - l.start[t]) * (W * N);
-  Vec u[N];
+  Cursor c = cursor(l, t, u0 + T::rank(), log);
   if (behind_one_another(l, t, u0, W * N, log)) {
-    const char* p = static_cast<const char*>(l.ptr[0][t]) + (u0 + T::rank()) * 16;
     char* q = static_cast<char*>(l.ptr[1][t]) + (u0 + T::rank()) * 16;
-#pragma unroll
-    for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
-    Cursor c = cursor(l, t, u0 + T::rank(), log);
     Place<2> e;
     e.align = 1;
+    e.off[1] = 0;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      scale_vec(u[k], scale, dt);
       e.valid = c.col == c.per_row - 1 ? l.cols[t] - static_cast<int>(c.col << log) : 1 << log;
-      e.off[1] = 0;
       store_vec(u[k], q + k * W * 16, e, 1, log);
       advance(l, t, c, W);
     }
     return;
   }
-  Place<2> p[N];
-  Cursor c = cursor(l, t, u0 + T::rank(), log);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    p[k] = place(l, t, c, log);
-    load_vec(u[k], l.ptr[0][t], p[k], 0, log);
+    store_vec(u[k], l.ptr[1][t], place(l, t, c, log), 1, log);
     advance(l, t, c, W);
   }
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    scale_vec(u[k], scale, dt);
-    store_vec(u[k], l.ptr[1][t], p[k], 1, log);
-  }
 }
 
-// Scales the chunks of a group's run, from its last one to its first: these are what reading the
-// run for the norm left in L2.
-template <class T, int N, class L>
-GNS_DEV void clip_chunks(const L& l, int group, int groups, float scale) {
-  const Run run = run_of(l, group, groups);
-  if (run.begin >= run.end) return;
-  int t = find_tensor(l, run.end - 1, 0, l.count - 1);
-  for (int chunk = run.end - 1; chunk >= run.begin; --chunk) {
-    while (l.start[t] > chunk) --t;
-    clip_chunk<T, N>(l, t, chunk, l.type[t] & 3, scale);
-  }
-}
-
-// Every block forms the norm from the slots (a few KB, in L2), which saves a launch.
+// Every block forms the norm from the slots (a few KB, in L2), which saves a launch. The chunks go
+// from the list's end to its start, all blocks near one another: a block with a run of its own, as
+// in norm_kernel, takes 4 % longer where memory is written too.
 template <class L>
-__global__ void __launch_bounds__(THREADS, L::kRows ? CLIP_ROW_BLOCKS : CLIP_BLOCKS) clip_kernel(const __grid_constant__ L l, Finish f, int first,
-                                                                   int in_place) {
+__global__ void __launch_bounds__(THREADS, L::kRows ? CLIP_ROW_BLOCKS : CLIP_BLOCKS)
+    clip_kernel(const __grid_constant__ L l, Finish f, int first, int in_place) {
   grid_dep_wait();
   float norm, scale;
   finish_norm<false>(f, &norm, &scale);
@@ -860,25 +814,54 @@ __global__ void __launch_bounds__(THREADS, L::kRows ? CLIP_ROW_BLOCKS : CLIP_BLO
   int t = l.count - 1;
   for (int chunk = l.start[l.count] - 1 - static_cast<int>(blockIdx.x); chunk >= 0; chunk -= gridDim.x) {
     if (l.start[t] > chunk) t = find_tensor(l, chunk, 0, t - 1);
-    clip_chunk<Block, CLIP_VEC>(l, t, chunk, l.type[t] & 3, scale);
+    const int dt = l.type[t] & 3, log = vec_log(dt);
+    const Place<2> e = edge_place<Block, CLIP_VEC>(l, t, chunk, log);
+    Vec u[CLIP_VEC], h;
+    if (e.valid) load_vec(h, l.ptr[0][t], e, 0, log);
+    load_chunk<Block>(l, t, chunk, log, u);
+#pragma unroll
+    for (int k = 0; k < CLIP_VEC; ++k) scale_vec(u[k], scale, dt);
+    store_chunk<Block>(l, t, chunk, log, u);
+    if (e.valid) {
+      scale_vec(h, scale, dt);
+      store_vec(h, l.ptr[1][t], e, 1, log);
+    }
   }
 }
 
 // ---------------------------------------------------------------------------------------
-// short lists: the whole call in one launch of one cluster
+// clipping a short list: the whole call in one launch of one cluster
 
-// A chunk is 2 KB here, for a warp, so that a list of small tensors spreads over many warps; the
-// blocks' shares meet in shared memory. Compared with the kernels above this saves the slots'
-// way through L2 and, in clipping, a launch; one cluster streams 1 MB in about the time of that.
-constexpr int SHORT_THREADS = 512, SHORT_VEC = 4, SHORT_CLUSTER = 8, SHORT_CHUNKS = 512;
+// A chunk is 4 KB here and every chunk has a warp of its own, which keeps it in registers between
+// its sum and the scaled store: the list is read once. The blocks' shares meet in shared memory.
+// What this saves is a launch on the host: a call takes 8.2 us where the two kernels above take 12
+// (both about 5.3 us on the GPU, at 0.2 MB); the norm alone is one launch anyway.
+constexpr int SHORT_THREADS = 512, SHORT_VEC = 8, SHORT_CLUSTER = 8;
+constexpr int SHORT_CHUNKS = SHORT_CLUSTER * SHORT_THREADS / 32;
 
-template <bool INF, bool CLIP, class L>
-__global__ void __launch_bounds__(SHORT_THREADS) short_kernel(const __grid_constant__ L l, Finish f, int in_place) {
+template <bool INF, class L>
+__global__ void __launch_bounds__(SHORT_THREADS) short_clip_kernel(const __grid_constant__ L l, Finish f, int in_place) {
   __shared__ alignas(8) Share share[SHORT_CLUSTER];
-  constexpr int warps = SHORT_THREADS / 32;
-  const int blocks = gridDim.x, group = blockIdx.x * warps + (threadIdx.x >> 5), groups = blocks * warps;
+  const int blocks = gridDim.x, chunk = blockIdx.x * (SHORT_THREADS / 32) + (threadIdx.x >> 5);
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  const Share s = block_share<INF, Warp, SHORT_VEC, SHORT_THREADS>(l, group, groups);
+  const bool mine = chunk < l.start[l.count];
+  const int t = mine ? find_tensor(l, chunk, 0, l.count - 1) : 0, dt = l.type[t] & 3, log = vec_log(dt);
+  Vec u[SHORT_VEC] = {}, h[1] = {};
+  Place<L::kRoles> e;
+  e.valid = 0;
+  if (mine) {
+    e = edge_place<Warp, SHORT_VEC>(l, t, chunk, log);
+    if (e.valid) load_vec(h[0], l.ptr[0][t], e, 0, log);
+    load_chunk<Warp>(l, t, chunk, log, u);
+  }
+  Share s;
+  if (INF) {
+    s = {__uint_as_float(block_max<SHORT_THREADS>(max(largest(u, dt), largest(h, dt)))), 0};
+  } else {
+    const uint32_t bits = bits_of(u) | bits_of(h);
+    s = square_share<SHORT_THREADS>(
+        [&](float pre, auto scaled) { return squares<scaled.value>(u, pre, dt) + squares<scaled.value>(h, pre, dt); }, bits);
+  }
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every block of the cluster runs
   if (static_cast<int>(threadIdx.x) < blocks) {
     const uint32_t to = mapa_shared(smem_u32(&share[blockIdx.x]), threadIdx.x);
@@ -895,14 +878,26 @@ __global__ void __launch_bounds__(SHORT_THREADS) short_kernel(const __grid_const
   for (int b = 0; b < blocks; ++b) n += scaled_share(share[b], top);
   norm_and_scale(f, INF ? __uint_as_float(most) : n, INF ? 0 : top, &norm, &scale);
   if (blockIdx.x == 0) write_result(f, norm, scale);
-  if constexpr (CLIP) {
-    if (in_place && scale == 1.f) return;
-    clip_chunks<Warp, SHORT_VEC>(l, group, groups, scale);
+  if (!mine || (in_place && scale == 1.f)) return;
+#pragma unroll
+  for (int k = 0; k < SHORT_VEC; ++k) scale_vec(u[k], scale, dt);
+  store_chunk<Warp>(l, t, chunk, log, u);
+  if (e.valid) {
+    scale_vec(h[0], scale, dt);
+    store_vec(h[0], l.ptr[1][t], e, 1, log);
   }
 }
 
 // ---------------------------------------------------------------------------------------
-// AdamW; roles: W, G, M, V, master. Type bits 0-1: W, 2-3: G, 4: has a master.
+// AdamW; roles: W, G, M, V, master
+//
+// m <- beta1 m + (1 - beta1) c g;  v <- beta2 v + (1 - beta2) (c g)^2
+// w <- (1 - lr wd) w - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+//
+// 22 to 28 bytes an element: HBM bounds it (6.5 TB/s read and written on 524 M weights, 96 % of a
+// copy's rate), with the root and the quotient hidden behind the loads of the other blocks. The
+// moments and masters stay in f32: a 16-bit v loses (1 - beta2) g^2 to rounding. A 16-bit weight is
+// rounded once, from f32. Types are looked at when the loads are out, so one launch takes any mix.
 
 struct AdamwArgs {
   float beta1, one_minus_beta1, beta2, one_minus_beta2;
@@ -933,8 +928,7 @@ GNS_DEV void adamw_unit(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[
   }
 }
 
-// The elements of one role of a unit; those that do not exist read as zero. align 2: the unit
-// starts on 8 elements' bytes, 1: on 16 bytes.
+// The elements of one role of a unit; those that do not exist read as zero.
 GNS_DEV void load_unit(Unit& u, const void* base, const Place<5>& p, int r, bool f32) {
   const int valid = p.valid;
   const bool whole = p.align && (valid == 8 || (p.over && valid));
@@ -997,9 +991,11 @@ GNS_DEV void store_unit(const Unit& u, void* base, const Place<5>& p, int r, boo
   }
 }
 
+// Blocks stride over the list (a run for each took 4 % longer) and find a chunk's tensor by halving:
+// one step may pass a hundred tensors.
 template <class L>
-__global__ void __launch_bounds__(THREADS, L::kRows ? ADAMW_ROW_BLOCKS : ADAMW_BLOCKS) adamw_kernel(const __grid_constant__ L l,
-                                                                     const __grid_constant__ AdamwArgs a) {
+__global__ void __launch_bounds__(THREADS, L::kRows ? ADAMW_ROW_BLOCKS : ADAMW_BLOCKS)
+    adamw_kernel(const __grid_constant__ L l, const __grid_constant__ AdamwArgs a) {
   const int total = l.start[l.count];
   AdamwStep s;
   s.scale = a.grad_scale ? *a.grad_scale : 1.f;
@@ -1073,11 +1069,12 @@ int check_tensor(const gns_tensor& t, const char* what, int i) {
   constexpr int64_t most = int64_t(1) << 40;
   if (x.count > most || x.rows > most || x.cols > most || x.rows > most / x.count || x.cols > most / (x.count * x.rows))
     return fail(GNS_ERR_INVALID, what, i, "more than 2^40 elements");
-  if (x.rows > 1 && (x.ld < x.cols || x.ld > most)) return fail(GNS_ERR_INVALID, what, i, "ld must lie in [cols, 2^40]");
+  if (x.rows > 1 && (x.ld < x.cols || x.ld > most / x.rows))
+    return fail(GNS_ERR_INVALID, what, i, "ld must be at least cols, and a matrix span at most 2^40 elements");
   if (x.count > 1) {
     const int64_t last = x.rows > 1 ? (x.rows - 1) * x.ld : 0;
-    if (x.rows > 1 && x.ld > most / x.rows) return fail(GNS_ERR_INVALID, what, i, "a matrix spans more than 2^40 elements");
-    if (x.stride < last + x.cols || x.stride > most) return fail(GNS_ERR_INVALID, what, i, "stride: matrices overlap, or lie over 2^40 elements apart");
+    if (x.stride < last + x.cols || x.stride > most / x.count)
+      return fail(GNS_ERR_INVALID, what, i, "stride: matrices overlap, or span more than 2^40 elements");
   }
   if (!flat(t) && (x.count * x.rows > 0x7fffffff || x.cols > 0x7fffffff))
     return fail(GNS_ERR_UNSUPPORTED, what, i, "rows with a pitch: at most 2^31 - 1 rows and columns");
@@ -1108,8 +1105,7 @@ struct Roles {
   }
 };
 
-// Fills entry k of a launch's list with tensor i; the number of its units of `unit` elements. A
-// unit is one 16-byte vector of the norm and of clipping, and 8 elements of AdamW.
+// Fills entry k of a launch's list with tensor i; returns the number of its units.
 template <int R, int CAP>
 int64_t put(FlatList<R, CAP>* l, int k, const Roles& a, int i) {
   const gns_batch& x = a.role[0][i].x;
@@ -1180,9 +1176,9 @@ int64_t put(RowList<R, CAP>* l, int k, const Roles& a, int i) {
   const int64_t per_row = (x.cols + (1 << log) - 1) >> log;
   l->by_row[k] = inverse(per_row);
   l->rows[k] = even ? 0 : static_cast<int>(x.rows);
-  bool tight = R < 5 && even && on16;
-  for (int r = 0; r < R; ++r) tight &= l->ld[r][k] == per_row << log;
-  if (tight) l->align[k] = TIGHT;
+  bool tight = even && on16;
+  for (int r = 0; r < R; ++r) tight &= !a.has(r, i) || l->ld[r][k] == per_row << log;
+  l->tight[k] = tight;
   l->by_matrix[k] = inverse(x.rows);
   return x.count * x.rows * per_row;
 }
@@ -1242,6 +1238,7 @@ enum How { ALONE, BEHIND, CLUSTER };
 
 template <class... P, class... A>
 int launch(const char* what, void (*kernel)(P...), int grid, void* stream, How how, const A&... args) {
+  static_assert((std::is_same_v<P, A> && ...), "arguments go by address");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = {};
   if (how == CLUSTER) {
@@ -1257,8 +1254,9 @@ int launch(const char* what, void (*kernel)(P...), int grid, void* stream, How h
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = &attr;
   cfg.numAttrs = how == ALONE ? 0 : 1;
+  void* at[] = {const_cast<void*>(static_cast<const void*>(&args))...};
   profile_count_launch();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), at);
   if (e == cudaSuccess) return GNS_OK;
   (void)cudaGetLastError();
   return set_error(GNS_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
@@ -1281,20 +1279,20 @@ int short_list(const Roles& a, int tensors, F f) {
   return l.count == tensors && l.start[l.count] <= SHORT_CHUNKS ? f(l) : 1;
 }
 
-template <int R, class F>
+template <class F>
 int short_lists(const Roles& a, int tensors, F f) {
   if (a.n > SMALL_LIST) return 1;
   int64_t total = 0;
   for (int i = 0; i < a.n; ++i) {
     const gns_tensor& t = a.role[0][i];
     total += t.x.count * t.x.rows * t.x.cols * size_of(t.dtype);
-    if (total > SHORT_CHUNKS * 2048) return 1;
+    if (total > SHORT_CHUNKS * SHORT_VEC * 512) return 1;
   }
-  const int rc = short_list<FlatList<R, SMALL_LIST>>(a, tensors, f);
-  return rc <= 0 ? rc : short_list<RowList<R, SMALL_LIST>>(a, tensors, f);
+  const int rc = short_list<FlatList<2, SMALL_LIST>>(a, tensors, f);
+  return rc <= 0 ? rc : short_list<RowList<2, SMALL_LIST>>(a, tensors, f);
 }
 
-// Blocks of the cluster: one for each `warps` chunks, a power of two.
+// Blocks of the cluster, a power of two: a warp for each chunk.
 int short_blocks(int chunks) {
   int blocks = 1;
   while (blocks < SHORT_CLUSTER && blocks * (SHORT_THREADS / 32) < chunks) blocks *= 2;
@@ -1360,12 +1358,7 @@ int grad_norm(const gns_tensor* g, int n, int norm_type, float max_norm, float e
   const int inf = norm_type == GNS_NORM_INF, left = not_empty(g, n);
   Finish f = {static_cast<Slot*>(ws), call_number(), result, dev_status, 0, inf, max_norm, eps};
   if (!left) return launch("grad norm", no_norm_kernel, 1, stream, ALONE, f);
-  const int rc = short_lists<1>({{g}, 1, n}, left, [&](const auto& l) {
-    using L = std::decay_t<decltype(l)>;
-    return launch("grad norm", inf ? short_kernel<true, false, L> : short_kernel<false, false, L>,
-                  short_blocks(l.start[l.count]), stream, CLUSTER, l, f, 0);
-  });
-  return rc <= 0 ? rc : norm_launches(g, n, left, stream, true, &f);
+  return norm_launches(g, n, left, stream, true, &f);
 }
 
 int clip_grads(const gns_tensor* g, const gns_tensor* out, int n, int norm_type, float max_norm, float eps,
@@ -1386,9 +1379,9 @@ int clip_grads(const gns_tensor* g, const gns_tensor* out, int n, int norm_type,
   Finish f = {static_cast<Slot*>(ws), call_number(), result, dev_status, 0, inf, max_norm, eps};
   if (!left) return launch("clip", no_norm_kernel, 1, stream, ALONE, f);
   const Roles a = {{g, out ? out : g}, 2, n};
-  int rc = short_lists<2>(a, left, [&](const auto& l) {
+  int rc = short_lists(a, left, [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
-    return launch("clip", inf ? short_kernel<true, true, L> : short_kernel<false, true, L>,
+    return launch("clip", inf ? short_clip_kernel<true, L> : short_clip_kernel<false, L>,
                   short_blocks(l.start[l.count]), stream, CLUSTER, l, f, in_place);
   });
   if (rc <= 0) return rc;
