@@ -50,9 +50,13 @@ constexpr int MAX_GRID = 1216;  // blocks of one launch at most
 // 4 and 4 560, 2 and 5 550, 8 and 3 562; rows with a pitch 4 and 4 (63 us for 112 MB; 4 and 3 69, 2
 // and 5 75).
 constexpr int NORM_VEC = 8, NORM_BLOCKS = 4, CLIP_VEC = 4, CLIP_BLOCKS = 3, CLIP_ROW_BLOCKS = 4;
-// AdamW takes one unit of 8 elements a thread: 524 M bf16 weights with masters in 2.25 ms with 3
-// blocks, 2.39 with 4, 2.69 with 2; rows with a pitch 157 us with 3, 144 with 4.
-constexpr int ADAMW_BLOCKS = 3, ADAMW_ROW_BLOCKS = 4;
+// AdamW takes one unit of 8 elements a thread, 128 threads a block. With its reads and writes mixed
+// more in flight is not faster on long lists: 524 M bf16 weights with masters 2.21 ms with 4 blocks,
+// 2.27 with 5, 2.30 with 6, 2.49 with 3, and 66 M 277, 284, 292 and 313 us; while 10 M in 120 tensors
+// take 45, 41, 39 and 51 us. So a launch of 2^15 chunks (34 M elements) or more has 4 blocks a SM, and a
+// shorter one 6 (between 4 M and 128 M aligned elements the two are within 2.5 %). Rows with a pitch,
+// where more has to be worked out before the loads, take 7 (28 M: 129 us; 6: 141).
+constexpr int ADAMW_THREADS = 128, ADAMW_BLOCKS = 6, ADAMW_LONG_BLOCKS = 4, ADAMW_ROW_BLOCKS = 7, ADAMW_LONG = 1 << 15;
 
 // ---------------------------------------------------------------------------------------
 // lists as kernel parameters (at most 32,764 bytes of parameters a launch)
@@ -915,6 +919,21 @@ struct AdamwStep {
   float scale, step_size, rsqrt_bc2;
 };
 
+// The hardware's root and reciprocal, each within 2^-23 of the exact one. The correctly rounded ones
+// leave their fast path for zeros and subnormals, and an embedding is full of them: rows that no
+// token has touched have v = 0, and m falls below 2^-126 some 800 steps after the last gradient (64
+// MB of bf16 embeddings of which 70 % get no gradient: 304 us against 285).
+GNS_DEV float approx_sqrt(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+GNS_DEV float approx_reciprocal(float x) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 GNS_DEV void adamw_unit(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[8], const AdamwArgs& a,
                         const AdamwStep& s, int valid, bool* bad) {
 #pragma unroll
@@ -922,8 +941,8 @@ GNS_DEV void adamw_unit(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[
     const float ge = g[e] * s.scale;
     m[e] = fmaf(a.beta1, m[e], a.one_minus_beta1 * ge);
     v[e] = fmaf(a.beta2, v[e], a.one_minus_beta2 * ge * ge);
-    const float denom = fmaf(sqrtf(v[e]), s.rsqrt_bc2, a.eps);
-    w[e] = fmaf(-s.step_size, m[e] / denom, a.decay * w[e]);
+    const float denom = fmaf(approx_sqrt(v[e]), s.rsqrt_bc2, a.eps);
+    w[e] = fmaf(-s.step_size, m[e] * approx_reciprocal(denom), a.decay * w[e]);
     *bad |= e < valid && !isfinite(w[e]);
   }
 }
@@ -994,7 +1013,7 @@ GNS_DEV void store_unit(const Unit& u, void* base, const Place<5>& p, int r, boo
 // Blocks stride over the list (a run for each took 4 % longer) and find a chunk's tensor by halving:
 // one step may pass a hundred tensors.
 template <class L>
-__global__ void __launch_bounds__(THREADS, L::kRows ? ADAMW_ROW_BLOCKS : ADAMW_BLOCKS)
+__global__ void __launch_bounds__(ADAMW_THREADS, L::kRows ? ADAMW_ROW_BLOCKS : ADAMW_BLOCKS)
     adamw_kernel(const __grid_constant__ L l, const __grid_constant__ AdamwArgs a) {
   const int total = l.start[l.count];
   AdamwStep s;
@@ -1010,7 +1029,7 @@ __global__ void __launch_bounds__(THREADS, L::kRows ? ADAMW_ROW_BLOCKS : ADAMW_B
   int t = 0;
   for (int chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
     if (l.start[t + 1] <= chunk) t = find_tensor(l, chunk, t + 1, l.count - 1);
-    const Place<5> p = place(l, t, static_cast<long long>(chunk - l.start[t]) * THREADS + threadIdx.x, 3);
+    const Place<5> p = place(l, t, static_cast<long long>(chunk - l.start[t]) * ADAMW_THREADS + threadIdx.x, 3);
     if (!p.valid) continue;
     const int wt = l.type[t] & 3, gt = (l.type[t] >> 2) & 3;
     const bool master = l.type[t] & 16;
@@ -1058,6 +1077,12 @@ bool flat(const gns_tensor& t) {
   return (x.rows == 1 || x.ld == x.cols) && (x.count == 1 || x.stride == x.rows * x.cols);
 }
 
+// Whether a b <= 2^40 (a, b > 0); no division, as there are five lists of hundreds of tensors.
+bool product(int64_t a, int64_t b) {
+  int64_t p;
+  return !__builtin_mul_overflow(a, b, &p) && p <= int64_t(1) << 40;
+}
+
 int check_tensor(const gns_tensor& t, const char* what, int i) {
   const gns_batch& x = t.x;
   if (t.dtype != GNS_BF16 && t.dtype != GNS_F16 && t.dtype != GNS_F32) return fail(GNS_ERR_INVALID, what, i, "unknown dtype");
@@ -1066,14 +1091,12 @@ int check_tensor(const gns_tensor& t, const char* what, int i) {
   if (!x.ptr) return fail(GNS_ERR_INVALID, what, i, "null data pointer");
   if (reinterpret_cast<uintptr_t>(x.ptr) % size_of(t.dtype))
     return fail(GNS_ERR_INVALID, what, i, "pointer must be aligned to an element");
-  constexpr int64_t most = int64_t(1) << 40;
-  if (x.count > most || x.rows > most || x.cols > most || x.rows > most / x.count || x.cols > most / (x.count * x.rows))
-    return fail(GNS_ERR_INVALID, what, i, "more than 2^40 elements");
-  if (x.rows > 1 && (x.ld < x.cols || x.ld > most / x.rows))
+  if (!product(x.count, x.rows) || !product(x.count * x.rows, x.cols)) return fail(GNS_ERR_INVALID, what, i, "more than 2^40 elements");
+  if (x.rows > 1 && (x.ld < x.cols || !product(x.ld, x.rows)))
     return fail(GNS_ERR_INVALID, what, i, "ld must be at least cols, and a matrix span at most 2^40 elements");
   if (x.count > 1) {
     const int64_t last = x.rows > 1 ? (x.rows - 1) * x.ld : 0;
-    if (x.stride < last + x.cols || x.stride > most / x.count)
+    if (x.stride < last + x.cols || !product(x.stride, x.count))
       return fail(GNS_ERR_INVALID, what, i, "stride: matrices overlap, or span more than 2^40 elements");
   }
   if (!flat(t) && (x.count * x.rows > 0x7fffffff || x.cols > 0x7fffffff))
@@ -1231,13 +1254,12 @@ int each_list(const Roles& a, int64_t chunk_units, F f) {
   return GNS_OK;
 }
 
-// ALONE: an ordinary launch of THREADS threads a block. BEHIND: one that may begin while the one
-// ahead of it on the stream ends, and waits for it itself (grid_dep_wait) before it touches memory.
-// CLUSTER: one cluster of SHORT_THREADS threads a block.
+// ALONE: an ordinary launch. BEHIND: one that may begin while the one ahead of it on the stream
+// ends, and waits for it itself (grid_dep_wait) before it touches memory. CLUSTER: one cluster.
 enum How { ALONE, BEHIND, CLUSTER };
 
 template <class... P, class... A>
-int launch(const char* what, void (*kernel)(P...), int grid, void* stream, How how, const A&... args) {
+int launch(const char* what, void (*kernel)(P...), int grid, int threads, void* stream, How how, const A&... args) {
   static_assert((std::is_same_v<P, A> && ...), "arguments go by address");
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr = {};
@@ -1250,7 +1272,7 @@ int launch(const char* what, void (*kernel)(P...), int grid, void* stream, How h
     attr.val.programmaticStreamSerializationAllowed = 1;
   }
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(how == CLUSTER ? SHORT_THREADS : THREADS);
+  cfg.blockDim = dim3(threads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = &attr;
   cfg.numAttrs = how == ALONE ? 0 : 1;
@@ -1345,11 +1367,11 @@ int norm_launches(const gns_tensor* g, int n, int left, void* stream, bool finis
     Slot* at = f->slots + f->nslots;
     f->nslots += grid;
     left -= l.count;
-    return launch("grad norm", f->inf ? norm_kernel<true, L> : norm_kernel<false, L>, grid, stream, ALONE, l, at, *f,
+    return launch("grad norm", f->inf ? norm_kernel<true, L> : norm_kernel<false, L>, grid, THREADS, stream, ALONE, l, at, *f,
                   static_cast<int>(finish && !left));
   };
   const int rc = each_list<FlatList<1, NORM_FLAT>>(a, THREADS * NORM_VEC, go);
-  return rc ? rc : each_list<RowList<1, NORM_ROWS>>(a, THREADS * NORM_VEC, go);
+  return rc || !left ? rc : each_list<RowList<1, NORM_ROWS>>(a, THREADS * NORM_VEC, go);
 }
 
 int grad_norm(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, float* result, void* ws,
@@ -1357,7 +1379,7 @@ int grad_norm(const gns_tensor* g, int n, int norm_type, float max_norm, float e
   if (int rc = check_norm(g, n, norm_type, max_norm, eps, result, ws, ws_bytes)) return rc;
   const int inf = norm_type == GNS_NORM_INF, left = not_empty(g, n);
   Finish f = {static_cast<Slot*>(ws), call_number(), result, dev_status, 0, inf, max_norm, eps};
-  if (!left) return launch("grad norm", no_norm_kernel, 1, stream, ALONE, f);
+  if (!left) return launch("grad norm", no_norm_kernel, 1, THREADS, stream, ALONE, f);
   return norm_launches(g, n, left, stream, true, &f);
 }
 
@@ -1375,26 +1397,29 @@ int clip_grads(const gns_tensor* g, const gns_tensor* out, int n, int norm_type,
     else if ((g[i].x.rows > 1 && g[i].x.ld != out[i].x.ld) || (g[i].x.count > 1 && g[i].x.stride != out[i].x.stride))
       return fail(GNS_ERR_INVALID, "outs", i, "may alias its gradient only with the same layout");
   }
-  const int inf = norm_type == GNS_NORM_INF, left = not_empty(g, n);
+  const int inf = norm_type == GNS_NORM_INF;
+  int left = not_empty(g, n);
   Finish f = {static_cast<Slot*>(ws), call_number(), result, dev_status, 0, inf, max_norm, eps};
-  if (!left) return launch("clip", no_norm_kernel, 1, stream, ALONE, f);
+  if (!left) return launch("clip", no_norm_kernel, 1, THREADS, stream, ALONE, f);
   const Roles a = {{g, out ? out : g}, 2, n};
   int rc = short_lists(a, left, [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
     return launch("clip", inf ? short_clip_kernel<true, L> : short_clip_kernel<false, L>,
-                  short_blocks(l.start[l.count]), stream, CLUSTER, l, f, in_place);
+                  short_blocks(l.start[l.count]), SHORT_THREADS, stream, CLUSTER, l, f, in_place);
   });
   if (rc <= 0) return rc;
   if ((rc = norm_launches(g, n, left, stream, false, &f))) return rc;
   int first = 1;  // the launch that writes the result
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
-    const int rc = launch("clip", clip_kernel<L>, grid_for(l.start[l.count], L::kRows ? CLIP_ROW_BLOCKS : CLIP_BLOCKS), stream, BEHIND, l, f, first, in_place);
+    const int grid = grid_for(l.start[l.count], L::kRows ? CLIP_ROW_BLOCKS : CLIP_BLOCKS);
+    const int rc = launch("clip", clip_kernel<L>, grid, THREADS, stream, BEHIND, l, f, first, in_place);
     first = 0;
+    left -= l.count;
     return rc;
   };
   rc = each_list<FlatList<2, CLIP_FLAT>>(a, THREADS * CLIP_VEC, go);
-  return rc ? rc : each_list<RowList<2, CLIP_ROWS>>(a, THREADS * CLIP_VEC, go);
+  return rc || !left ? rc : each_list<RowList<2, CLIP_ROWS>>(a, THREADS * CLIP_VEC, go);
 }
 
 int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, const gns_tensor* V,
@@ -1442,12 +1467,16 @@ int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, co
   a.step = step_count;
   a.status = dev_status;
   const Roles lists = {{W, G, M, V, master}, 5, n};
+  int left = not_empty(W, n);
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
-    return launch("AdamW", adamw_kernel<L>, grid_for(l.start[l.count], L::kRows ? ADAMW_ROW_BLOCKS : ADAMW_BLOCKS), stream, ALONE, l, a);
+    const int chunks = l.start[l.count];
+    const int grid = grid_for(chunks, L::kRows ? ADAMW_ROW_BLOCKS : chunks < ADAMW_LONG ? ADAMW_BLOCKS : ADAMW_LONG_BLOCKS);
+    left -= l.count;
+    return launch("AdamW", adamw_kernel<L>, grid, ADAMW_THREADS, stream, ALONE, l, a);
   };
-  int rc = each_list<FlatList<5, ADAMW_FLAT>>(lists, THREADS, go);
-  return rc ? rc : each_list<RowList<5, ADAMW_ROWS>>(lists, THREADS, go);
+  int rc = each_list<FlatList<5, ADAMW_FLAT>>(lists, ADAMW_THREADS, go);
+  return rc || !left ? rc : each_list<RowList<5, ADAMW_ROWS>>(lists, ADAMW_THREADS, go);
 }
 
 // A C caller gets a status whatever happens: the only exception these calls can raise is a
