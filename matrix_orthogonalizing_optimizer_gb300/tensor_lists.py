@@ -220,8 +220,7 @@ class AdamWParams:
     step: int = 1
 
     def c_struct(self) -> GnsAdamwParams:
-        return GnsAdamwParams(float(self.lr), float(self.beta1), float(self.beta2), float(self.eps),
-                              float(self.weight_decay), int(self.step))
+        return GnsAdamwParams(self.lr, self.beta1, self.beta2, self.eps, self.weight_decay, self.step)
 
 
 def adamw_step(W, G, M, V, lr: Optional[float] = None, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,

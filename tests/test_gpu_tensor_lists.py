@@ -267,6 +267,19 @@ def test_clip_non_finite():
     assert torch.isnan(t).all()
 
 
+@pytest.mark.parametrize("values", [(1e30,), (1e-30,), (1e25, 1e-30, 1.0), (3e-12, 1e-30), (1e-44,), (0.0,)])
+@pytest.mark.parametrize("n", [5, 3000, 200003])
+def test_clip_of_extreme_values(values, n):
+    """Short lists and long ones take different kernels: both keep squares out of f32's range right."""
+    ts = [torch.full((n,), v, device="cuda") for v in values] + [torch.zeros(7, device="cuda")]
+    before = [t.clone() for t in ts]
+    want = _norm64(ts)
+    r = gns.clip_grads(ts, 0.25 * want, eps=0.0)
+    assert abs(float(r[0]) - want) <= NORM_TOL * want + 2.0 ** -150
+    for t, b in zip(ts, before):
+        assert torch.equal(_bits(t), _bits(_scaled(b, r[1])))
+
+
 # ------------------------------------------------------------------------------------ AdamW
 
 P = dict(lr=1e-2, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.1)
@@ -499,6 +512,52 @@ def test_captured_clip_and_step_match_eager():
         for x, y in zip(a, b):
             # the corrections 1 - beta^t are formed on the device: a few units in the last place apart
             assert float((x.double() - y.double()).abs().max()) <= 2.0 ** (-7 if x.dtype == BF else -18) * max(1e-3, float(x.double().abs().max()))
+
+
+def test_replayed_norm_reads_the_gradients_anew():
+    """A captured norm gives the gradients' norm at each replay, not an earlier one's."""
+    ts = _make("large", BF, 3) + _make("pitched", F32, 4)
+    result = torch.empty(2, device="cuda")
+    work = gns.alloc_workspace(gns.list_workspace_size(len(ts)), "cuda")
+    status = _status()
+    gns.grad_norm(ts, result=result, workspace=work, status=status)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gns.grad_norm(ts, result=result, workspace=work, status=status)
+    first = _norm64(ts)
+    for k in range(1, 30):
+        torch._foreach_mul_(ts, 2.0 if k % 3 else 0.25)
+        graph.replay()
+        want = first * 2.0 ** (k - 3 * (k // 3))
+        assert abs(float(result[0]) - want) <= NORM_TOL * want, k
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("kind", ["sizes", "large", "many", "many_pitched"])
+def test_calls_in_a_row_share_a_workspace(kind):
+    """Nothing waits between the calls, and the workspace holds whatever was there before."""
+    ts = _make(kind, BF, 6)
+    work = gns.alloc_workspace(gns.list_workspace_size(len(ts)), "cuda")
+    work.fill_(255)
+    results = torch.empty(60, 2, device="cuda")
+    outs = _copies(ts)
+    status = _status()
+    lists, out_lists = gns.tensor_list(ts), gns.tensor_list(outs)
+    for k in range(60):
+        if k % 2:
+            gns.grad_norm(lists, result=results[k], workspace=work, status=status)
+        else:
+            gns.clip_grads(lists, math.inf, outs=out_lists, result=results[k], workspace=work, status=status)
+        torch._foreach_mul_(ts, 2.0 if k % 4 < 2 else 0.5)
+    got = results[:, 0].tolist()
+    assert int(status) == 0
+    want = got[1]  # after one doubling
+    for k, x in enumerate(got):
+        expected = want * (0.5, 1.0, 2.0, 1.0)[k % 4]
+        if kind == "sizes" and k % 2 == 0:  # the short list's clipping adds in another order
+            assert abs(x - expected) <= NORM_TOL * expected
+        else:
+            assert x == expected, k  # the same order, values times a power of two: the same bits
 
 
 def test_another_stream():
