@@ -52,31 +52,32 @@ constexpr int MAX_GRID = 1216;  // blocks of one launch at most
 constexpr int NORM_VEC = 8, NORM_BLOCKS = 4, CLIP_VEC = 4, CLIP_BLOCKS = 3, CLIP_ROW_BLOCKS = 4;
 // AdamW takes one unit of 8 elements a thread, 128 threads a block. With its reads and writes mixed
 // more in flight is not faster on long lists: 524 M bf16 weights with masters 2.21 ms with 4 blocks,
-// 2.27 with 5, 2.30 with 6, 2.49 with 3, and 66 M 277, 284, 292 and 313 us; while 10 M in 120 tensors
-// take 45, 41, 39 and 51 us. So a launch of 2^15 chunks (34 M elements) or more has 4 blocks a SM, and a
-// shorter one 6 (between 4 M and 128 M aligned elements the two are within 2.5 %). Rows with a pitch,
-// where more has to be worked out before the loads, take 7 (28 M: 129 us; 6: 141).
-constexpr int ADAMW_THREADS = 128, ADAMW_BLOCKS = 6, ADAMW_LONG_BLOCKS = 4, ADAMW_ROW_BLOCKS = 7, ADAMW_LONG = 1 << 15;
+// 2.27 with 5, 2.30 with 6, 2.49 with 3; 66 M 277, 284, 292 and 313 us; 28 M 121, 124 and 129 us with 4,
+// 5 and 6; while 10 M in 120 tensors take 45, 41 and 39 us. So a launch of 2^14 chunks (17 M elements) or
+// more has 4 blocks a SM, a shorter one 6. Rows with a pitch, where more has to be worked out before
+// the loads, have 7 (28 M: 129 us; 6: 141).
+constexpr int ADAMW_THREADS = 128, ADAMW_BLOCKS = 6, ADAMW_LONG_BLOCKS = 4, ADAMW_ROW_BLOCKS = 7, ADAMW_LONG = 1 << 14;
 
 // ---------------------------------------------------------------------------------------
 // lists as kernel parameters (at most 32,764 bytes of parameters a launch)
 
-// start[i]: the launch's first chunk of tensor i, start[count]: all chunks. type: the GNS_ types
-// of roles 0 and 1 in bits 0-1 and 2-3, bit 4 set when the tensor has a master (AdamW's role 4).
-// align: 2 = every unit starts on 8 elements' bytes in every role, 1 = on 16 bytes, 0 = on an
-// element.
+// start[i]: the launch's first chunk of tensor i, start[count]: all chunks. What else is known of a
+// tensor lies together, as constant memory is read by lines. type: the GNS_ types of roles 0 and 1
+// in bits 0-1 and 2-3, bit 4 set when the tensor has a master (AdamW's role 4). align: 2 = every
+// unit starts on 8 elements' bytes in every role, 1 = on 16 bytes, 0 = on an element.
 template <int R, int CAP>
 struct FlatList {
   template <int C>
   using Cap = FlatList<R, C>;
   static constexpr bool kRows = false;
   static constexpr int kRoles = R, kCap = CAP;
-  void* ptr[R][CAP];
-  long long n[CAP];
+  struct Tensor {
+    void* ptr[R];
+    long long n;
+    unsigned char type, align;
+    unsigned char head;  // elements before the first unit
+  } at[CAP];
   int start[CAP + 1];
-  unsigned char type[CAP];
-  unsigned char align[CAP];
-  unsigned char head[CAP];  // elements before the first unit
   int count;
 };
 
@@ -86,19 +87,20 @@ struct RowList {
   using Cap = RowList<R, C>;
   static constexpr bool kRows = true;
   static constexpr int kRoles = R, kCap = CAP;
-  void* ptr[R][CAP];
-  long long ld[R][CAP], stride[R][CAP];
-  int nrows[CAP];  // of all matrices
-  int rows[CAP];   // of one matrix; 0: rows lie evenly from the first matrix to the last
-  int cols[CAP];
-  // 2^64 / d + 1 for the units of a row and the rows of a matrix (0: d is 1)
-  unsigned long long by_row[CAP], by_matrix[CAP];
+  struct Tensor {
+    void* ptr[R];
+    long long ld[R], stride[R];
+    // 2^64 / d + 1 for the units of a row and the rows of a matrix (0: d is 1)
+    unsigned long long by_row, by_matrix;
+    int nrows;  // of all matrices
+    int rows;   // of one matrix; 0: rows lie evenly from the first matrix to the last
+    int cols;
+    unsigned char type, align;
+    // rows on 16 bytes whose pitch is their own length up to the next unit, from the first matrix
+    // to the last, in every role (as empty_padded makes them): units lie behind one another
+    unsigned char tight;
+  } at[CAP];
   int start[CAP + 1];
-  unsigned char type[CAP];
-  unsigned char align[CAP];
-  // rows on 16 bytes whose pitch is their own length up to the next unit, from the first matrix to
-  // the last, in every role (as empty_padded makes them): units lie behind one another
-  unsigned char tight[CAP];
   int count;
 };
 
@@ -188,40 +190,44 @@ GNS_DEV int find_tensor(const L& l, int chunk, int lo, int hi) {
 }
 
 // A unit of 2^log elements in every role: one vector of the norm and of clipping (log 2 or 3), 8
-// elements of AdamW. off: its first element. valid: how many of its elements exist, from the first
-// on (0: no unit). align: as in the list. over: what lies behind the valid elements up to the end
-// of a vector can be read too.
+// elements of AdamW. off: its first element, step: from one element to the next. valid: how many of
+// its elements exist, from the first on (0: no unit). align: as in the list. over: what lies behind
+// the valid elements up to the end of a vector can be read too.
 template <int R>
 struct Place {
   long long off[R];
-  int valid, align;
+  int valid, align, step;
   bool over;
 };
 
 // A flat tensor has whole units from element `head` on; what lies before and behind them, fewer
-// than 2 units, follows as units of one element. Where no head puts every role on a vector the
-// units count from its first element, and the last may be short.
+// than 2 units, follows as units of one element. Where no head puts every role on a vector, 32 units
+// share 32 << log elements, each with every 32nd of them, so that a warp's accesses to single
+// elements lie side by side.
 template <int R, int CAP>
 GNS_DEV Place<R> place(const FlatList<R, CAP>& l, int t, long long unit, int log) {
   Place<R> p;
   long long o = unit << log;
-  const long long n = l.n[t];
-  if (l.align[t]) {
-    const int head = l.head[t];
+  const long long n = l.at[t].n;
+  if (l.at[t].align) {
+    const int head = l.at[t].head;
     const long long whole = (n - head) >> log;
     if (unit < whole) {
       o += head;
       p.valid = 1 << log;
-      p.align = l.align[t];
+      p.align = l.at[t].align;
     } else {
       const long long e = unit - whole;  // of n - whole units' edge elements
       o = e < head ? e : e + (whole << log);
       p.valid = o < n;
       p.align = 0;
     }
+    p.step = 1;
   } else {
-    p.valid = static_cast<int>(max(0ll, min(n - o, 1ll << log)));
+    o = ((unit >> 5) << (log + 5)) + (unit & 31);
+    p.valid = static_cast<int>(max(0ll, min((n - o + 31) >> 5, 1ll << log)));
     p.align = 0;
+    p.step = 32;
   }
   p.over = false;
 #pragma unroll
@@ -245,15 +251,15 @@ struct Cursor {
 template <int R, int CAP>
 GNS_DEV Cursor cursor(const RowList<R, CAP>& l, int t, unsigned long long unit, int log) {
   Cursor c;
-  c.per_row = (static_cast<uint32_t>(l.cols[t]) + (1u << log) - 1u) >> log;
+  c.per_row = (static_cast<uint32_t>(l.at[t].cols) + (1u << log) - 1u) >> log;
   // a tensor of 2^32 units or more needs the division
-  c.row = (unit >> 32) == 0 ? quotient(static_cast<uint32_t>(unit), l.by_row[t]) : unit / c.per_row;
+  c.row = (unit >> 32) == 0 ? quotient(static_cast<uint32_t>(unit), l.at[t].by_row) : unit / c.per_row;
   c.col = static_cast<uint32_t>(unit - c.row * c.per_row);
   return c;
 }
 template <int R, int CAP>
 GNS_DEV void advance(const RowList<R, CAP>& l, int t, Cursor& c, uint32_t step) {
-  const uint32_t q = step < c.per_row ? 0u : quotient(step, l.by_row[t]);
+  const uint32_t q = step < c.per_row ? 0u : quotient(step, l.at[t].by_row);
   c.row += q;
   c.col += step - q * c.per_row;
   if (c.col >= c.per_row) {
@@ -265,19 +271,20 @@ GNS_DEV void advance(const RowList<R, CAP>& l, int t, Cursor& c, uint32_t step) 
 template <int R, int CAP>
 GNS_DEV Place<R> place(const RowList<R, CAP>& l, int t, const Cursor& c, int log) {
   Place<R> p;
-  const uint32_t nrows = static_cast<uint32_t>(l.nrows[t]), at = c.col << log;
-  p.valid = c.row < nrows ? static_cast<int>(min(1u << log, static_cast<uint32_t>(l.cols[t]) - at)) : 0;
-  p.align = l.align[t];
+  const uint32_t nrows = static_cast<uint32_t>(l.at[t].nrows), at = c.col << log;
+  p.valid = c.row < nrows ? static_cast<int>(min(1u << log, static_cast<uint32_t>(l.at[t].cols) - at)) : 0;
+  p.align = l.at[t].align;
+  p.step = 1;
   // on 16 bytes a row's pitch holds its last vector whole; behind the last row there may be nothing
   p.over = c.row + 1 < nrows;
   const uint32_t row = static_cast<uint32_t>(c.row);
-  if (l.rows[t]) {
-    const uint32_t b = quotient(row, l.by_matrix[t]), i = row - b * static_cast<uint32_t>(l.rows[t]);
+  if (l.at[t].rows) {
+    const uint32_t b = quotient(row, l.at[t].by_matrix), i = row - b * static_cast<uint32_t>(l.at[t].rows);
 #pragma unroll
-    for (int r = 0; r < R; ++r) p.off[r] = b * l.stride[r][t] + i * l.ld[r][t] + at;
+    for (int r = 0; r < R; ++r) p.off[r] = b * l.at[t].stride[r] + i * l.at[t].ld[r] + at;
   } else {
 #pragma unroll
-    for (int r = 0; r < R; ++r) p.off[r] = row * l.ld[r][t] + at;
+    for (int r = 0; r < R; ++r) p.off[r] = row * l.at[t].ld[r] + at;
   }
   return p;
 }
@@ -339,19 +346,19 @@ GNS_DEV void keep(Vec& u, int valid, int log) {
 // The elements of one role of a unit; those that do not exist read as zero.
 template <int R>
 GNS_DEV void load_vec(Vec& u, const void* base, const Place<R>& p, int r, int log) {
-  const int valid = p.valid;
+  const int valid = p.valid, step = p.step;
   if (p.align && (valid == 1 << log || (p.over && valid))) {
     ld_v4(u.w, static_cast<const char*>(base) + (p.off[r] << (4 - log)));
     if (valid != 1 << log) keep(u, valid, log);
   } else if (log == 2) {
     const uint32_t* q = static_cast<const uint32_t*>(base) + p.off[r];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) u.w[e] = e < valid ? q[e] : 0u;
+    for (int e = 0; e < 4; ++e) u.w[e] = e < valid ? q[e * step] : 0u;
   } else {
     const unsigned short* q = static_cast<const unsigned short*>(base) + p.off[r];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = 2 * e < valid ? q[2 * e] : 0u, hi = 2 * e + 1 < valid ? q[2 * e + 1] : 0u;
+      const uint32_t lo = 2 * e < valid ? q[2 * e * step] : 0u, hi = 2 * e + 1 < valid ? q[(2 * e + 1) * step] : 0u;
       u.w[e] = lo | (hi << 16);
     }
   }
@@ -359,19 +366,19 @@ GNS_DEV void load_vec(Vec& u, const void* base, const Place<R>& p, int r, int lo
 
 template <int R>
 GNS_DEV void store_vec(const Vec& u, void* base, const Place<R>& p, int r, int log) {
-  const int valid = p.valid;
+  const int valid = p.valid, step = p.step;
   if (p.align && valid == 1 << log) {
     st_v4(static_cast<char*>(base) + (p.off[r] << (4 - log)), u.w);
   } else if (log == 2) {
     uint32_t* q = static_cast<uint32_t*>(base) + p.off[r];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (e < valid) q[e] = u.w[e];
+      if (e < valid) q[e * step] = u.w[e];
   } else {
     unsigned short* q = static_cast<unsigned short*>(base) + p.off[r];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < valid) q[e] = static_cast<unsigned short>(u.w[e / 2] >> (16 * (e & 1)));
+      if (e < valid) q[e * step] = static_cast<unsigned short>(u.w[e / 2] >> (16 * (e & 1)));
   }
 }
 
@@ -392,13 +399,13 @@ template <class T, int N, int R, int CAP>
 GNS_DEV void load_chunk(const FlatList<R, CAP>& l, int t, int chunk, int log, Vec (&u)[N]) {
   constexpr int W = T::kThreads;
   const long long u0 = static_cast<long long>(chunk - l.start[t]) * (W * N);
-  if (R > 1 && !l.align[t]) {
+  if (R > 1 && !l.at[t].align) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) load_vec(u[k], l.ptr[0][t], place(l, t, u0 + k * W + T::rank(), log), 0, log);
+    for (int k = 0; k < N; ++k) load_vec(u[k], l.at[t].ptr[0], place(l, t, u0 + k * W + T::rank(), log), 0, log);
     return;
   }
-  const char* p = static_cast<const char*>(l.ptr[0][t]) + ((l.head[t] + (u0 << log)) << (4 - log)) + T::rank() * 16;
-  const long long whole = ((l.n[t] - l.head[t]) >> log) - u0;
+  const char* p = static_cast<const char*>(l.at[t].ptr[0]) + ((l.at[t].head + (u0 << log)) << (4 - log)) + T::rank() * 16;
+  const long long whole = ((l.at[t].n - l.at[t].head) >> log) - u0;
   if (whole >= W * N) {
 #pragma unroll
     for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
@@ -418,10 +425,10 @@ template <class T, int N, int R, int CAP>
 GNS_DEV Place<R> edge_place(const FlatList<R, CAP>& l, int t, int chunk, int log) {
   constexpr int W = T::kThreads;
   const long long u0 = static_cast<long long>(chunk - l.start[t]) * (W * N);
-  const long long whole = ((l.n[t] - l.head[t]) >> log) - u0;
+  const long long whole = ((l.at[t].n - l.at[t].head) >> log) - u0;
   Place<R> p;
   p.valid = 0;
-  if (whole < W * N && l.align[t]) {
+  if (whole < W * N && l.at[t].align) {
     // units whole, whole + 1, ... of this chunk: the first of them that is this thread's turn
     const int first = max(static_cast<int>(whole), 0);
     const int unit = first + ((T::rank() - first) & (W - 1));
@@ -440,8 +447,8 @@ GNS_DEV Place<R> edge_place(const RowList<R, CAP>&, int, int, int) {
 // unit of tight rows, so that only what each row's last vector holds has to be looked at.
 template <int R, int CAP>
 GNS_DEV bool behind_one_another(const RowList<R, CAP>& l, int t, unsigned long long u0, int n, int log) {
-  const unsigned long long per_row = (static_cast<uint32_t>(l.cols[t]) + (1u << log) - 1u) >> log;
-  return l.tight[t] && u0 + n < per_row * static_cast<uint32_t>(l.nrows[t]);
+  const unsigned long long per_row = (static_cast<uint32_t>(l.at[t].cols) + (1u << log) - 1u) >> log;
+  return l.at[t].tight && u0 + n < per_row * static_cast<uint32_t>(l.at[t].nrows);
 }
 
 template <class T, int N, int R, int CAP>
@@ -449,11 +456,11 @@ GNS_DEV void load_chunk(const RowList<R, CAP>& l, int t, int chunk, int log, Vec
   constexpr int W = T::kThreads;
   const unsigned long long u0 = static_cast<unsigned long long>(chunk - l.start[t]) * (W * N);
   if (behind_one_another(l, t, u0, W * N, log)) {
-    const char* p = static_cast<const char*>(l.ptr[0][t]) + (u0 + T::rank()) * 16;
+    const char* p = static_cast<const char*>(l.at[t].ptr[0]) + (u0 + T::rank()) * 16;
 #pragma unroll
     for (int k = 0; k < N; ++k) ld_v4(u[k].w, p + k * W * 16);
     Cursor c = cursor(l, t, u0 + T::rank(), log);
-    const int last = l.cols[t] - static_cast<int>((c.per_row - 1) << log);
+    const int last = l.at[t].cols - static_cast<int>((c.per_row - 1) << log);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       if (c.col == c.per_row - 1) keep(u[k], last, log);
@@ -464,7 +471,7 @@ GNS_DEV void load_chunk(const RowList<R, CAP>& l, int t, int chunk, int log, Vec
   Cursor c = cursor(l, t, u0 + T::rank(), log);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    load_vec(u[k], l.ptr[0][t], place(l, t, c, log), 0, log);
+    load_vec(u[k], l.at[t].ptr[0], place(l, t, c, log), 0, log);
     advance(l, t, c, W);
   }
 }
@@ -479,10 +486,10 @@ GNS_DEV void for_vectors(const L& l, F f) {
   int t = find_tensor(l, begin, 0, l.count - 1);
   for (int chunk = begin; chunk < end; ++chunk) {
     while (l.start[t + 1] <= chunk) ++t;
-    const int dt = l.type[t] & 3, log = vec_log(dt);
+    const int dt = l.at[t].type & 3, log = vec_log(dt);
     const auto p = edge_place<Block, NORM_VEC>(l, t, chunk, log);
     Vec u[NORM_VEC], h[1];
-    if (p.valid) load_vec(h[0], l.ptr[0][t], p, 0, log);
+    if (p.valid) load_vec(h[0], l.at[t].ptr[0], p, 0, log);
     load_chunk<Block>(l, t, chunk, log, u);
     f(u, dt);
     if (p.valid) f(h, dt);
@@ -761,13 +768,13 @@ template <class T, int N, int CAP>
 GNS_DEV void store_chunk(const FlatList<2, CAP>& l, int t, int chunk, int log, const Vec (&u)[N]) {
   constexpr int W = T::kThreads;
   const long long u0 = static_cast<long long>(chunk - l.start[t]) * (W * N);
-  if (!l.align[t]) {
+  if (!l.at[t].align) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) store_vec(u[k], l.ptr[1][t], place(l, t, u0 + k * W + T::rank(), log), 1, log);
+    for (int k = 0; k < N; ++k) store_vec(u[k], l.at[t].ptr[1], place(l, t, u0 + k * W + T::rank(), log), 1, log);
     return;
   }
-  char* q = static_cast<char*>(l.ptr[1][t]) + ((l.head[t] + (u0 << log)) << (4 - log)) + T::rank() * 16;
-  const long long whole = ((l.n[t] - l.head[t]) >> log) - u0;
+  char* q = static_cast<char*>(l.at[t].ptr[1]) + ((l.at[t].head + (u0 << log)) << (4 - log)) + T::rank() * 16;
+  const long long whole = ((l.at[t].n - l.at[t].head) >> log) - u0;
   if (whole >= W * N) {
 #pragma unroll
     for (int k = 0; k < N; ++k) st_v4(q + k * W * 16, u[k].w);
@@ -785,13 +792,13 @@ GNS_DEV void store_chunk(const RowList<2, CAP>& l, int t, int chunk, int log, co
   const unsigned long long u0 = static_cast<unsigned long long>(chunk - l.start[t]) * (W * N);
   Cursor c = cursor(l, t, u0 + T::rank(), log);
   if (behind_one_another(l, t, u0, W * N, log)) {
-    char* q = static_cast<char*>(l.ptr[1][t]) + (u0 + T::rank()) * 16;
+    char* q = static_cast<char*>(l.at[t].ptr[1]) + (u0 + T::rank()) * 16;
     Place<2> e;
-    e.align = 1;
+    e.align = e.step = 1;
     e.off[1] = 0;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      e.valid = c.col == c.per_row - 1 ? l.cols[t] - static_cast<int>(c.col << log) : 1 << log;
+      e.valid = c.col == c.per_row - 1 ? l.at[t].cols - static_cast<int>(c.col << log) : 1 << log;
       store_vec(u[k], q + k * W * 16, e, 1, log);
       advance(l, t, c, W);
     }
@@ -799,7 +806,7 @@ GNS_DEV void store_chunk(const RowList<2, CAP>& l, int t, int chunk, int log, co
   }
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    store_vec(u[k], l.ptr[1][t], place(l, t, c, log), 1, log);
+    store_vec(u[k], l.at[t].ptr[1], place(l, t, c, log), 1, log);
     advance(l, t, c, W);
   }
 }
@@ -818,17 +825,17 @@ __global__ void __launch_bounds__(THREADS, L::kRows ? CLIP_ROW_BLOCKS : CLIP_BLO
   int t = l.count - 1;
   for (int chunk = l.start[l.count] - 1 - static_cast<int>(blockIdx.x); chunk >= 0; chunk -= gridDim.x) {
     if (l.start[t] > chunk) t = find_tensor(l, chunk, 0, t - 1);
-    const int dt = l.type[t] & 3, log = vec_log(dt);
+    const int dt = l.at[t].type & 3, log = vec_log(dt);
     const Place<2> e = edge_place<Block, CLIP_VEC>(l, t, chunk, log);
     Vec u[CLIP_VEC], h;
-    if (e.valid) load_vec(h, l.ptr[0][t], e, 0, log);
+    if (e.valid) load_vec(h, l.at[t].ptr[0], e, 0, log);
     load_chunk<Block>(l, t, chunk, log, u);
 #pragma unroll
     for (int k = 0; k < CLIP_VEC; ++k) scale_vec(u[k], scale, dt);
     store_chunk<Block>(l, t, chunk, log, u);
     if (e.valid) {
       scale_vec(h, scale, dt);
-      store_vec(h, l.ptr[1][t], e, 1, log);
+      store_vec(h, l.at[t].ptr[1], e, 1, log);
     }
   }
 }
@@ -849,13 +856,13 @@ __global__ void __launch_bounds__(SHORT_THREADS) short_clip_kernel(const __grid_
   const int blocks = gridDim.x, chunk = blockIdx.x * (SHORT_THREADS / 32) + (threadIdx.x >> 5);
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const bool mine = chunk < l.start[l.count];
-  const int t = mine ? find_tensor(l, chunk, 0, l.count - 1) : 0, dt = l.type[t] & 3, log = vec_log(dt);
+  const int t = mine ? find_tensor(l, chunk, 0, l.count - 1) : 0, dt = l.at[t].type & 3, log = vec_log(dt);
   Vec u[SHORT_VEC] = {}, h[1] = {};
   Place<L::kRoles> e;
   e.valid = 0;
   if (mine) {
     e = edge_place<Warp, SHORT_VEC>(l, t, chunk, log);
-    if (e.valid) load_vec(h[0], l.ptr[0][t], e, 0, log);
+    if (e.valid) load_vec(h[0], l.at[t].ptr[0], e, 0, log);
     load_chunk<Warp>(l, t, chunk, log, u);
   }
   Share s;
@@ -888,7 +895,7 @@ __global__ void __launch_bounds__(SHORT_THREADS) short_clip_kernel(const __grid_
   store_chunk<Warp>(l, t, chunk, log, u);
   if (e.valid) {
     scale_vec(h[0], scale, dt);
-    store_vec(h[0], l.ptr[1][t], e, 1, log);
+    store_vec(h[0], l.at[t].ptr[1], e, 1, log);
   }
 }
 
@@ -949,7 +956,7 @@ GNS_DEV void adamw_unit(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[
 
 // The elements of one role of a unit; those that do not exist read as zero.
 GNS_DEV void load_unit(Unit& u, const void* base, const Place<5>& p, int r, bool f32) {
-  const int valid = p.valid;
+  const int valid = p.valid, step = p.step;
   const bool whole = p.align && (valid == 8 || (p.over && valid));
   if (f32) {
     const uint32_t* q = static_cast<const uint32_t*>(base) + p.off[r];
@@ -960,7 +967,7 @@ GNS_DEV void load_unit(Unit& u, const void* base, const Place<5>& p, int r, bool
       if (valid > 4) ld_v4(u.w + 4, q + 4);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) u.w[e] = e < valid ? q[e] : 0u;
+      for (int e = 0; e < 8; ++e) u.w[e] = e < valid ? q[e * step] : 0u;
     }
     if (whole && valid != 8) {
 #pragma unroll
@@ -977,7 +984,7 @@ GNS_DEV void load_unit(Unit& u, const void* base, const Place<5>& p, int r, bool
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = 2 * e < valid ? q[2 * e] : 0u, hi = 2 * e + 1 < valid ? q[2 * e + 1] : 0u;
+        const uint32_t lo = 2 * e < valid ? q[2 * e * step] : 0u, hi = 2 * e + 1 < valid ? q[(2 * e + 1) * step] : 0u;
         u.w[e] = lo | (hi << 16);
       }
     }
@@ -985,7 +992,7 @@ GNS_DEV void load_unit(Unit& u, const void* base, const Place<5>& p, int r, bool
 }
 
 GNS_DEV void store_unit(const Unit& u, void* base, const Place<5>& p, int r, bool f32) {
-  const int valid = p.valid;
+  const int valid = p.valid, step = p.step;
   if (f32) {
     uint32_t* q = static_cast<uint32_t*>(base) + p.off[r];
     if (valid == 8 && p.align == 2) {
@@ -996,7 +1003,7 @@ GNS_DEV void store_unit(const Unit& u, void* base, const Place<5>& p, int r, boo
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < valid) q[e] = u.w[e];
+        if (e < valid) q[e * step] = u.w[e];
     }
   } else {
     unsigned short* q = static_cast<unsigned short*>(base) + p.off[r];
@@ -1005,7 +1012,7 @@ GNS_DEV void store_unit(const Unit& u, void* base, const Place<5>& p, int r, boo
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < valid) q[e] = static_cast<unsigned short>(u.w[e / 2] >> (16 * (e & 1)));
+        if (e < valid) q[e * step] = static_cast<unsigned short>(u.w[e / 2] >> (16 * (e & 1)));
     }
   }
 }
@@ -1031,16 +1038,16 @@ __global__ void __launch_bounds__(ADAMW_THREADS, L::kRows ? ADAMW_ROW_BLOCKS : A
     if (l.start[t + 1] <= chunk) t = find_tensor(l, chunk, t + 1, l.count - 1);
     const Place<5> p = place(l, t, static_cast<long long>(chunk - l.start[t]) * ADAMW_THREADS + threadIdx.x, 3);
     if (!p.valid) continue;
-    const int wt = l.type[t] & 3, gt = (l.type[t] >> 2) & 3;
-    const bool master = l.type[t] & 16;
+    const int wt = l.at[t].type & 3, gt = (l.at[t].type >> 2) & 3;
+    const bool master = l.at[t].type & 16;
     Unit uw, ug, um, uv;
     if (master)
-      load_unit(uw, l.ptr[4][t], p, 4, true);
+      load_unit(uw, l.at[t].ptr[4], p, 4, true);
     else
-      load_unit(uw, l.ptr[0][t], p, 0, wt == GNS_F32);
-    load_unit(ug, l.ptr[1][t], p, 1, gt == GNS_F32);
-    load_unit(um, l.ptr[2][t], p, 2, true);
-    load_unit(uv, l.ptr[3][t], p, 3, true);
+      load_unit(uw, l.at[t].ptr[0], p, 0, wt == GNS_F32);
+    load_unit(ug, l.at[t].ptr[1], p, 1, gt == GNS_F32);
+    load_unit(um, l.at[t].ptr[2], p, 2, true);
+    load_unit(uv, l.at[t].ptr[3], p, 3, true);
     float w[8], g[8], m[8], v[8];
     unpack(w, uw, master ? (int)GNS_F32 : wt);
     unpack(g, ug, gt);
@@ -1048,15 +1055,15 @@ __global__ void __launch_bounds__(ADAMW_THREADS, L::kRows ? ADAMW_ROW_BLOCKS : A
     unpack(v, uv, GNS_F32);
     adamw_unit(w, g, m, v, a, s, p.valid, &bad);
     pack(um, m, GNS_F32);
-    store_unit(um, l.ptr[2][t], p, 2, true);
+    store_unit(um, l.at[t].ptr[2], p, 2, true);
     pack(uv, v, GNS_F32);
-    store_unit(uv, l.ptr[3][t], p, 3, true);
+    store_unit(uv, l.at[t].ptr[3], p, 3, true);
     if (master) {
       pack(um, w, GNS_F32);
-      store_unit(um, l.ptr[4][t], p, 4, true);
+      store_unit(um, l.at[t].ptr[4], p, 4, true);
     }
     pack(uw, w, wt);
-    store_unit(uw, l.ptr[0][t], p, 0, wt == GNS_F32);
+    store_unit(uw, l.at[t].ptr[0], p, 0, wt == GNS_F32);
   }
   if (bad) set_status(a.status, GNS_DEVST_NONFINITE);
 }
@@ -1164,12 +1171,12 @@ int64_t put(FlatList<R, CAP>* l, int k, const Roles& a, int i) {
   }
   if (!align) head = 0;
   if (head > n) head = static_cast<int>(n);
-  l->n[k] = n;
-  l->head[k] = static_cast<unsigned char>(head);
-  l->align[k] = static_cast<unsigned char>(align);
+  l->at[k].n = n;
+  l->at[k].head = static_cast<unsigned char>(head);
+  l->at[k].align = static_cast<unsigned char>(align);
   const int log = vectors && a.role[0][i].dtype == GNS_F32 ? 2 : 3;
   const int64_t whole = (n - head) >> log;
-  return align ? whole + (n - (whole << log)) : (n + (1 << log) - 1) >> log;
+  return align ? whole + (n - (whole << log)) : (n + (32 << log) - 1) >> (log + 5) << 5;
 }
 
 uint64_t inverse(int64_t d) { return d > 1 ? ~uint64_t(0) / static_cast<uint64_t>(d) + 1 : 0; }
@@ -1177,32 +1184,32 @@ uint64_t inverse(int64_t d) { return d > 1 ? ~uint64_t(0) / static_cast<uint64_t
 template <int R, int CAP>
 int64_t put(RowList<R, CAP>* l, int k, const Roles& a, int i) {
   const gns_batch& x = a.role[0][i].x;
-  l->nrows[k] = static_cast<int>(x.count * x.rows);
+  l->at[k].nrows = static_cast<int>(x.count * x.rows);
   bool even = true;  // matrices follow one another at their rows' pitch
-  l->cols[k] = static_cast<int>(x.cols);
+  l->at[k].cols = static_cast<int>(x.cols);
   uint64_t bits16 = 0, bits32 = 0;  // low bits of every address and step in bytes, 16-bit and f32
   for (int r = 0; r < R; ++r) {
-    l->ld[r][k] = l->stride[r][k] = 0;
+    l->at[k].ld[r] = l->at[k].stride[r] = 0;
     if (!a.has(r, i)) continue;
     const gns_tensor& t = a.role[r][i];
-    if (t.x.rows > 1) l->ld[r][k] = t.x.ld;
-    if (t.x.count > 1) l->stride[r][k] = t.x.stride;
+    if (t.x.rows > 1) l->at[k].ld[r] = t.x.ld;
+    if (t.x.count > 1) l->at[k].stride[r] = t.x.stride;
     even &= t.x.count == 1 || t.x.rows == 1 || t.x.stride == t.x.rows * t.x.ld;
-    if (t.x.rows == 1) l->ld[r][k] = l->stride[r][k];
+    if (t.x.rows == 1) l->at[k].ld[r] = l->at[k].stride[r];
     const int es = size_of(t.dtype);
-    (es == 4 ? bits32 : bits16) |= reinterpret_cast<uintptr_t>(t.x.ptr) | static_cast<uint64_t>(l->ld[r][k] * es) |
-                                   static_cast<uint64_t>(l->stride[r][k] * es);
+    (es == 4 ? bits32 : bits16) |= reinterpret_cast<uintptr_t>(t.x.ptr) | static_cast<uint64_t>(l->at[k].ld[r] * es) |
+                                   static_cast<uint64_t>(l->at[k].stride[r] * es);
   }
   const bool on16 = ((bits16 | bits32) & 15) == 0;
-  l->align[k] = static_cast<unsigned char>(!on16 ? 0 : (bits32 & 31) ? 1 : 2);
+  l->at[k].align = static_cast<unsigned char>(!on16 ? 0 : (bits32 & 31) ? 1 : 2);
   const int log = R < 5 && a.role[0][i].dtype == GNS_F32 ? 2 : 3;
   const int64_t per_row = (x.cols + (1 << log) - 1) >> log;
-  l->by_row[k] = inverse(per_row);
-  l->rows[k] = even ? 0 : static_cast<int>(x.rows);
+  l->at[k].by_row = inverse(per_row);
+  l->at[k].rows = even ? 0 : static_cast<int>(x.rows);
   bool tight = even && on16;
-  for (int r = 0; r < R; ++r) tight &= !a.has(r, i) || l->ld[r][k] == per_row << log;
-  l->tight[k] = tight;
-  l->by_matrix[k] = inverse(x.rows);
+  for (int r = 0; r < R; ++r) tight &= !a.has(r, i) || l->at[k].ld[r] == per_row << log;
+  l->at[k].tight = tight;
+  l->at[k].by_matrix = inverse(x.rows);
   return x.count * x.rows * per_row;
 }
 
@@ -1218,8 +1225,8 @@ int fill(L* l, const Roles& a, int from, int64_t chunk_units) {
     const int64_t units = put(l, k, a, i);
     const int64_t c = (units + chunk_units - 1) / chunk_units;
     if (k && chunks + c > (1 << 30)) break;
-    for (int r = 0; r < L::kRoles; ++r) l->ptr[r][k] = a.has(r, i) ? a.role[r][i].x.ptr : nullptr;
-    l->type[k] = a.type(i);
+    for (int r = 0; r < L::kRoles; ++r) l->at[k].ptr[r] = a.has(r, i) ? a.role[r][i].x.ptr : nullptr;
+    l->at[k].type = a.type(i);
     l->start[k] = static_cast<int>(chunks);
     chunks += c;
     ++k;
@@ -1230,7 +1237,7 @@ int fill(L* l, const Roles& a, int from, int64_t chunk_units) {
 }
 
 // Lists of one launch: how many tensors its parameters hold.
-constexpr int SMALL_LIST = 64;
+constexpr int SMALL_LIST = 128;
 constexpr int NORM_FLAT = 1024, NORM_ROWS = 448, CLIP_FLAT = 768, CLIP_ROWS = 320, ADAMW_FLAT = 512, ADAMW_ROWS = 176;
 
 static_assert(sizeof(FlatList<1, NORM_FLAT>) < 32000 && sizeof(RowList<1, NORM_ROWS>) < 32000, "kernel parameters");

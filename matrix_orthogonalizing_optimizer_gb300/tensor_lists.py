@@ -243,9 +243,10 @@ def adamw_step(W, G, M, V, lr: Optional[float] = None, beta1: float = 0.9, beta2
         params = AdamWParams(lr, beta1, beta2, eps, weight_decay, step)
     if w.has_none:
         raise ValueError("every weight must be a tensor")
-    _same_layout("G", w, g)
-    _same_layout("M", w, m)
-    _same_layout("V", w, v)
+    if not w.layout_key == g.layout_key == m.layout_key == v.layout_key:
+        _same_layout("G", w, g)
+        _same_layout("M", w, m)
+        _same_layout("V", w, v)
     master_address = None
     if masters is not None:
         p = tensor_list(masters)
