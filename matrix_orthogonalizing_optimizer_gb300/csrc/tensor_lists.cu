@@ -404,7 +404,8 @@ GNS_DEV void load_chunk(const FlatList<R, CAP>& l, int t, int chunk, int log, Ve
     for (int k = 0; k < N; ++k) load_vec(u[k], l.at[t].ptr[0], place(l, t, u0 + k * W + T::rank(), log), 0, log);
     return;
   }
-  const char* p = static_cast<const char*>(l.at[t].ptr[0]) + ((l.at[t].head + (u0 << log)) << (4 - log)) + T::rank() * 16;
+  const char* p =
+      static_cast<const char*>(l.at[t].ptr[0]) + ((l.at[t].head + (u0 << log)) << (4 - log)) + T::rank() * 16;
   const long long whole = ((l.at[t].n - l.at[t].head) >> log) - u0;
   if (whole >= W * N) {
 #pragma unroll
@@ -481,7 +482,8 @@ GNS_DEV void load_chunk(const RowList<R, CAP>& l, int t, int chunk, int log, Vec
 template <class L, class F>
 GNS_DEV void for_vectors(const L& l, F f) {
   const long long total = l.start[l.count];
-  const int begin = static_cast<int>(total * blockIdx.x / gridDim.x), end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+  const int begin = static_cast<int>(total * blockIdx.x / gridDim.x);
+  const int end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
   if (begin >= end) return;
   int t = find_tensor(l, begin, 0, l.count - 1);
   for (int chunk = begin; chunk < end; ++chunk) {
@@ -851,7 +853,8 @@ constexpr int SHORT_THREADS = 512, SHORT_VEC = 8, SHORT_CLUSTER = 8;
 constexpr int SHORT_CHUNKS = SHORT_CLUSTER * SHORT_THREADS / 32;
 
 template <bool INF, class L>
-__global__ void __launch_bounds__(SHORT_THREADS) short_clip_kernel(const __grid_constant__ L l, Finish f, int in_place) {
+__global__ void __launch_bounds__(SHORT_THREADS)
+    short_clip_kernel(const __grid_constant__ L l, Finish f, int in_place) {
   __shared__ alignas(8) Share share[SHORT_CLUSTER];
   const int blocks = gridDim.x, chunk = blockIdx.x * (SHORT_THREADS / 32) + (threadIdx.x >> 5);
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -871,7 +874,8 @@ __global__ void __launch_bounds__(SHORT_THREADS) short_clip_kernel(const __grid_
   } else {
     const uint32_t bits = bits_of(u) | bits_of(h);
     s = square_share<SHORT_THREADS>(
-        [&](float pre, auto scaled) { return squares<scaled.value>(u, pre, dt) + squares<scaled.value>(h, pre, dt); }, bits);
+        [&](float pre, auto scaled) { return squares<scaled.value>(u, pre, dt) + squares<scaled.value>(h, pre, dt); },
+        bits);
   }
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every block of the cluster runs
   if (static_cast<int>(threadIdx.x) < blocks) {
@@ -1092,13 +1096,16 @@ bool product(int64_t a, int64_t b) {
 
 int check_tensor(const gns_tensor& t, const char* what, int i) {
   const gns_batch& x = t.x;
-  if (t.dtype != GNS_BF16 && t.dtype != GNS_F16 && t.dtype != GNS_F32) return fail(GNS_ERR_INVALID, what, i, "unknown dtype");
-  if (x.count < 0 || x.rows < 0 || x.cols < 0) return fail(GNS_ERR_INVALID, what, i, "count, rows and cols must be >= 0");
+  if (t.dtype != GNS_BF16 && t.dtype != GNS_F16 && t.dtype != GNS_F32)
+    return fail(GNS_ERR_INVALID, what, i, "unknown dtype");
+  if (x.count < 0 || x.rows < 0 || x.cols < 0)
+    return fail(GNS_ERR_INVALID, what, i, "count, rows and cols must be >= 0");
   if (empty(t)) return GNS_OK;
   if (!x.ptr) return fail(GNS_ERR_INVALID, what, i, "null data pointer");
-  if (reinterpret_cast<uintptr_t>(x.ptr) % size_of(t.dtype))
+  if (reinterpret_cast<uintptr_t>(x.ptr) & (size_of(t.dtype) - 1))
     return fail(GNS_ERR_INVALID, what, i, "pointer must be aligned to an element");
-  if (!product(x.count, x.rows) || !product(x.count * x.rows, x.cols)) return fail(GNS_ERR_INVALID, what, i, "more than 2^40 elements");
+  if (!product(x.count, x.rows) || !product(x.count * x.rows, x.cols))
+    return fail(GNS_ERR_INVALID, what, i, "more than 2^40 elements");
   if (x.rows > 1 && (x.ld < x.cols || !product(x.ld, x.rows)))
     return fail(GNS_ERR_INVALID, what, i, "ld must be at least cols, and a matrix span at most 2^40 elements");
   if (x.count > 1) {
@@ -1332,7 +1339,8 @@ int short_blocks(int chunks) {
 // not hold but by a chance of 2^-64: a mix of a counter that is a bijection of 64 bits (the finalizer
 // of SplitMix64, Steele, Lea and Flood 2014).
 uint64_t call_number() {
-  static const uint64_t seed = static_cast<uint64_t>(std::chrono::high_resolution_clock::now().time_since_epoch().count());
+  static const uint64_t seed =
+      static_cast<uint64_t>(std::chrono::high_resolution_clock::now().time_since_epoch().count());
   static std::atomic<uint64_t> calls{0};
   uint64_t z = (seed << 20) + ++calls;
   z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
@@ -1341,8 +1349,8 @@ uint64_t call_number() {
   return z ? z : 1;
 }
 
-int check_norm(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, const float* result, const void* ws,
-               size_t ws_bytes) {
+int check_norm(const gns_tensor* g, int n, int norm_type, float max_norm, float eps, const float* result,
+               const void* ws, size_t ws_bytes) {
   if (!g || !result) return set_error(GNS_ERR_INVALID, "null argument");
   if (n < 1) return set_error(GNS_ERR_INVALID, "need at least one tensor");
   if (norm_type != GNS_NORM_L2 && norm_type != GNS_NORM_INF) return set_error(GNS_ERR_INVALID, "unknown norm type");
@@ -1374,8 +1382,8 @@ int norm_launches(const gns_tensor* g, int n, int left, void* stream, bool finis
     Slot* at = f->slots + f->nslots;
     f->nslots += grid;
     left -= l.count;
-    return launch("grad norm", f->inf ? norm_kernel<true, L> : norm_kernel<false, L>, grid, THREADS, stream, ALONE, l, at, *f,
-                  static_cast<int>(finish && !left));
+    return launch("grad norm", f->inf ? norm_kernel<true, L> : norm_kernel<false, L>, grid, THREADS, stream, ALONE, l,
+                  at, *f, static_cast<int>(finish && !left));
   };
   const int rc = each_list<FlatList<1, NORM_FLAT>>(a, THREADS * NORM_VEC, go);
   return rc || !left ? rc : each_list<RowList<1, NORM_ROWS>>(a, THREADS * NORM_VEC, go);
@@ -1434,7 +1442,8 @@ int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, co
                const int32_t* step_count, int32_t* dev_status, void* stream) {
   if (!W || !G || !M || !V || !p) return set_error(GNS_ERR_INVALID, "null argument");
   if (n < 1) return set_error(GNS_ERR_INVALID, "need at least one tensor");
-  if (!std::isfinite(p->lr) || !std::isfinite(p->weight_decay)) return set_error(GNS_ERR_INVALID, "AdamW params must be finite");
+  if (!std::isfinite(p->lr) || !std::isfinite(p->weight_decay))
+    return set_error(GNS_ERR_INVALID, "AdamW params must be finite");
   if (!(p->beta1 >= 0.0 && p->beta1 < 1.0) || !(p->beta2 >= 0.0 && p->beta2 < 1.0))
     return set_error(GNS_ERR_INVALID, "beta1 and beta2 must be in [0, 1)");
   if (!(p->eps > 0.0) || !std::isfinite(p->eps)) return set_error(GNS_ERR_INVALID, "eps must be finite and > 0");
@@ -1454,7 +1463,8 @@ int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, co
       if (r == 4 && W[i].dtype == GNS_F32) return fail(GNS_ERR_INVALID, name[r], i, "an f32 weight takes no master");
       if (empty(t)) continue;
       for (int q = 0; q < r; ++q)
-        if (role[q] && role[q][i].x.ptr == t.x.ptr) return fail(GNS_ERR_INVALID, name[r], i, "W, G, M, V and master may not alias");
+        if (role[q] && role[q][i].x.ptr == t.x.ptr)
+          return fail(GNS_ERR_INVALID, name[r], i, "W, G, M, V and master may not alias");
     }
   }
   AdamwArgs a;
@@ -1478,7 +1488,8 @@ int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, co
   auto go = [&](const auto& l) {
     using L = std::decay_t<decltype(l)>;
     const int chunks = l.start[l.count];
-    const int grid = grid_for(chunks, L::kRows ? ADAMW_ROW_BLOCKS : chunks < ADAMW_LONG ? ADAMW_BLOCKS : ADAMW_LONG_BLOCKS);
+    const int flat_blocks = chunks < ADAMW_LONG ? ADAMW_BLOCKS : ADAMW_LONG_BLOCKS;
+    const int grid = grid_for(chunks, L::kRows ? ADAMW_ROW_BLOCKS : flat_blocks);
     left -= l.count;
     return launch("AdamW", adamw_kernel<L>, grid, ADAMW_THREADS, stream, ALONE, l, a);
   };
@@ -1514,7 +1525,8 @@ GNS_API size_t gns_list_workspace_size(int n) {
 
 GNS_API int gns_grad_norm(const gns_tensor* grads, int n, int norm_type, float max_norm, float eps, float* result,
                           void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
-  return guarded([&] { return grad_norm(grads, n, norm_type, max_norm, eps, result, ws, ws_bytes, dev_status, stream); });
+  return guarded(
+      [&] { return grad_norm(grads, n, norm_type, max_norm, eps, result, ws, ws_bytes, dev_status, stream); });
 }
 
 GNS_API int gns_clip_grads(const gns_tensor* grads, const gns_tensor* outs, int n, int norm_type, float max_norm,

@@ -22,7 +22,7 @@ import torch
 from . import _lib
 from ._lib import GnsAdamwParams, GnsTensor, load
 from ._lib import check as check_rc
-from .api import _CallStatus, _device_scalar, _dtype_code, alloc_workspace
+from .api import _CallStatus, _device_scalar, _dtype_code, _status_ptr, alloc_workspace
 
 
 # Field by field a descriptor costs ten times what one packed write does.
@@ -179,11 +179,14 @@ def grad_norm(grads, max_norm: Optional[float] = None, norm_type: float = 2.0, e
     g = tensor_list(grads)
     code = _norm_code(norm_type)
     result, ws = _norm_buffers(g, result, workspace, stream)
-    cs = _CallStatus(status, g.device, check, stream)
+    cs = _CallStatus(None, g.device, check, stream) if status is None else None
     rc = load().gns_grad_norm(g.address, len(g), code, math.inf if max_norm is None else float(max_norm), float(eps),
-                              result.data_ptr(), ws.data_ptr(), ws.numel(), cs.ptr(), _stream(stream, g.device))
-    check_rc(rc, "gns_grad_norm")
-    cs.done("gns_grad_norm")
+                              result.data_ptr(), ws.data_ptr(), ws.numel(), cs.ptr() if cs else _status_ptr(status),
+                              _stream(stream, g.device))
+    if rc:
+        check_rc(rc, "gns_grad_norm")
+    if cs:
+        cs.done("gns_grad_norm")
     return result
 
 
@@ -200,11 +203,14 @@ def clip_grads(grads, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6
         _same_layout("outs", g, o)
         out_address = o.address
     result, ws = _norm_buffers(g, result, workspace, stream)
-    cs = _CallStatus(status, g.device, check, stream)
+    cs = _CallStatus(None, g.device, check, stream) if status is None else None
     rc = load().gns_clip_grads(g.address, out_address, len(g), code, float(max_norm), float(eps), result.data_ptr(),
-                               ws.data_ptr(), ws.numel(), cs.ptr(), _stream(stream, g.device))
-    check_rc(rc, "gns_clip_grads")
-    cs.done("gns_clip_grads")
+                               ws.data_ptr(), ws.numel(), cs.ptr() if cs else _status_ptr(status),
+                               _stream(stream, g.device))
+    if rc:
+        check_rc(rc, "gns_clip_grads")
+    if cs:
+        cs.done("gns_clip_grads")
     return result
 
 
@@ -252,10 +258,12 @@ def adamw_step(W, G, M, V, lr: Optional[float] = None, beta1: float = 0.9, beta2
         p = tensor_list(masters)
         _same_layout("masters", w, p, optional=True)
         master_address = p.address
-    cs = _CallStatus(status, w.device, check, stream)
+    cs = _CallStatus(None, w.device, check, stream) if status is None else None
     rc = load().gns_adamw_step(w.address, g.address, m.address, v.address, master_address, len(w),
                                ctypes.byref(params.c_struct()), _device_scalar("grad_scale", grad_scale, torch.float32),
-                               _device_scalar("step_count", step_count, torch.int32), cs.ptr(),
-                               _stream(stream, w.device))
-    check_rc(rc, "gns_adamw_step")
-    cs.done("gns_adamw_step")
+                               _device_scalar("step_count", step_count, torch.int32),
+                               cs.ptr() if cs else _status_ptr(status), _stream(stream, w.device))
+    if rc:
+        check_rc(rc, "gns_adamw_step")
+    if cs:
+        cs.done("gns_adamw_step")
