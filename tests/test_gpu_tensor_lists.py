@@ -51,6 +51,9 @@ def _make(kind, dtype, seed, scale=1.0):
                 _randn((4, 9, 13), dtype, seed + 2, scale)[:, 1:7, 2:11], _randn((301, 9), dtype, seed + 3, scale)[:, :1],
                 _randn((5, 20011), dtype, seed + 4, scale)[:, 1:20009], _randn((6, 1, 24), dtype, seed + 5, scale)[:, :, :20],
                 _randn((7, 24), dtype, seed + 6, scale)[:1, 1:9]]
+    if kind == "pitched_stacks":  # rows on 16 bytes, matrices that do not follow at the rows' pitch
+        return [_randn((3, 20, 64), dtype, seed, scale)[:, :17, :53], _randn((5, 9, 32), dtype, seed + 1, scale)[:, :8, :],
+                _randn((2, 3, 4112), dtype, seed + 2, scale)[:, :2, :4100], _randn((4, 2, 2064), dtype, seed + 3, scale)[:, :1, :2057]]
     if kind == "many_pitched":
         return [_randn((3, 5), dtype, seed + i, scale)[:, :4] for i in range(520)]
     if kind == "shapes":  # scalars, empty tensors, more dimensions, other orders in memory
@@ -62,7 +65,7 @@ def _make(kind, dtype, seed, scale=1.0):
     raise ValueError(kind)
 
 
-KINDS = ["sizes", "offsets", "many", "pitched", "many_pitched", "shapes", "large"]
+KINDS = ["sizes", "offsets", "many", "pitched", "pitched_stacks", "many_pitched", "shapes", "large"]
 
 
 def _norm64(ts):
@@ -169,6 +172,22 @@ def test_norm_of_a_tensor_beyond_32_bits():
     r = gns.clip_grads([t], want / 2, eps=0.0)
     assert t[-1].item() == pytest.approx(1.5, rel=2.0 ** -8) and t[2 ** 31 + 4].item() == pytest.approx(1.0, rel=2.0 ** -8)
     assert float(r[1]) == pytest.approx(0.5, rel=2.0 ** -17)
+
+
+def test_pitched_rows_beyond_32_bits():
+    t = torch.zeros(70001, 40008, dtype=BF, device="cuda")[:, :40003]
+    t[-1, -3:] = 2.0
+    t[53700, 5] = 3.0  # near element 2^31
+    t[0, 0] = 1.0
+    want = math.sqrt(3 * 4 + 9 + 1)
+    assert abs(float(gns.grad_norm([t])[0]) - want) <= NORM_TOL * want
+    whole = torch.as_strided(t, (70001, 40008), (40008, 1))
+    whole[:, 40003:] = 7.0  # beside the rows
+    r = gns.clip_grads([t], want / 2, eps=0.0)
+    assert abs(float(r[0]) - want) <= NORM_TOL * want
+    half = torch.tensor(2.0, device="cuda").mul(r[1]).to(BF)
+    assert t[-1, -3:].tolist() == [half.item()] * 3 and float(t[53700, 5]) == float((3.0 * r[1]).to(BF))
+    assert bool((whole[:, 40003:] == 7.0).all())
 
 
 # ------------------------------------------------------------------------------------ clipping
@@ -366,7 +385,7 @@ TYPES = [(F32, F32, False), (BF, BF, False), (BF, BF, True), (BF, F32, False), (
 
 
 @pytest.mark.parametrize("wdt,gdt,master", TYPES)
-@pytest.mark.parametrize("kind", ["sizes", "offsets", "pitched", "shapes"])
+@pytest.mark.parametrize("kind", ["sizes", "offsets", "pitched", "pitched_stacks", "shapes"])
 def test_adamw(kind, wdt, gdt, master):
     _adamw_check(*_adamw_lists(kind, wdt, gdt, master), step=3)
 
@@ -530,6 +549,33 @@ def test_replayed_norm_reads_the_gradients_anew():
         graph.replay()
         want = first * 2.0 ** (k - 3 * (k // 3))
         assert abs(float(result[0]) - want) <= NORM_TOL * want, k
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("kind", ["sizes", "large", "pitched"])
+def test_replayed_clipping(kind):
+    """Clipping captured once: each replay clips the gradients that are there then."""
+    ts = _make(kind, BF, 9)
+    base = [t.clone() for t in ts]
+    outs = [torch.empty_like(t) for t in ts]
+    result = torch.empty(2, device="cuda")
+    work = gns.alloc_workspace(gns.list_workspace_size(len(ts)), "cuda")
+    status = _status()
+    lists = gns.tensor_list(ts), gns.tensor_list(outs)
+    max_norm = 0.5 * _norm64(ts)
+    call = lambda: gns.clip_grads(lists[0], max_norm, outs=lists[1], result=result, workspace=work, status=status)  # noqa: E731
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for factor in (1.0, 4.0, 0.25, 2.0):
+        for t, b in zip(ts, base):
+            t.copy_(b * factor)
+        graph.replay()
+        want = 2.0 * max_norm * factor
+        assert abs(float(result[0]) - want) <= NORM_TOL * want
+        for t, o in zip(ts, outs):
+            assert torch.equal(_bits(o), _bits(_scaled(t, result[1])))
     assert int(status) == 0
 
 
