@@ -54,13 +54,20 @@ def _describe(array, at: int, t: torch.Tensor):
             rows, cols = shape[-2:]
             _PACK(array, at, t.data_ptr(), math.prod(shape[:-2]), rows, cols, cols, rows * cols, code, 0)
         return shape
+    steps = t.stride()
+    if n == 2 and steps[1] == 1 and steps[0] >= shape[1]:
+        _PACK(array, at, t.data_ptr(), 1, shape[0], shape[1], steps[0], shape[0] * steps[0], code, 0)
+        return shape
+    if n == 3 and steps[2] == 1 and steps[1] >= shape[2] and steps[0] >= (shape[1] - 1) * steps[1] + shape[2]:
+        _PACK(array, at, t.data_ptr(), *shape, steps[1], steps[0], code, 0)
+        return shape
     order = tuple(sorted(range(n), key=lambda d: (-t.stride(d), -shape[d], d)))
     u = t.permute(order)
     if u.is_contiguous():
         _describe(array, at, u)
         return shape, order
     # leading dimensions that lie evenly behind one another are one
-    dims, steps = list(shape), list(t.stride())
+    dims, steps = list(shape), list(steps)
     while len(dims) > 3 and (dims[0] == 1 or steps[0] == steps[1] * dims[1]):
         d0 = dims.pop(0)
         steps.pop(0)
