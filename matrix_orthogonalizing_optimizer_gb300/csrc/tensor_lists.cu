@@ -946,7 +946,7 @@ GNS_DEV float approx_reciprocal(float x) {
 }
 
 GNS_DEV void adamw_unit(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[8], const AdamwArgs& a,
-                        const AdamwStep& s, int valid, bool* bad) {
+                        const AdamwStep& s) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float ge = g[e] * s.scale;
@@ -954,8 +954,25 @@ GNS_DEV void adamw_unit(float (&w)[8], float (&g)[8], float (&m)[8], float (&v)[
     v[e] = fmaf(a.beta2, v[e], a.one_minus_beta2 * ge * ge);
     const float denom = fmaf(approx_sqrt(v[e]), s.rsqrt_bc2, a.eps);
     w[e] = fmaf(-s.step_size, m[e] * approx_reciprocal(denom), a.decay * w[e]);
-    *bad |= e < valid && !isfinite(w[e]);
   }
+}
+
+// Whether a unit holds an infinity or a NaN as stored (a 16-bit weight may become one by its rounding):
+// an exponent of ones, to which one more in its lowest bit carries into the place of the sign.
+GNS_DEV bool not_finite(const Unit& u, int dt, int valid) {
+  uint32_t hit = 0;
+  if (dt == GNS_F32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) hit |= e < valid ? (u.w[e] & 0x7fffffffu) + 0x00800000u : 0u;
+    return hit >> 31;
+  }
+  const uint32_t one = dt == GNS_BF16 ? 0x00800080u : 0x04000400u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t exist = 2 * e + 1 < valid ? 0x80008000u : 2 * e < valid ? 0x8000u : 0u;
+    hit |= ((u.w[e] & 0x7fff7fffu) + one) & exist;
+  }
+  return hit != 0;
 }
 
 // The elements of one role of a unit; those that do not exist read as zero.
@@ -1057,7 +1074,7 @@ __global__ void __launch_bounds__(ADAMW_THREADS, L::kRows ? ADAMW_ROW_BLOCKS : A
     unpack(g, ug, gt);
     unpack(m, um, GNS_F32);
     unpack(v, uv, GNS_F32);
-    adamw_unit(w, g, m, v, a, s, p.valid, &bad);
+    adamw_unit(w, g, m, v, a, s);
     pack(um, m, GNS_F32);
     store_unit(um, l.at[t].ptr[2], p, 2, true);
     pack(uv, v, GNS_F32);
@@ -1067,6 +1084,7 @@ __global__ void __launch_bounds__(ADAMW_THREADS, L::kRows ? ADAMW_ROW_BLOCKS : A
       store_unit(um, l.at[t].ptr[4], p, 4, true);
     }
     pack(uw, w, wt);
+    bad |= not_finite(uw, wt, p.valid);
     store_unit(uw, l.at[t].ptr[0], p, 0, wt == GNS_F32);
   }
   if (bad) set_status(a.status, GNS_DEVST_NONFINITE);
