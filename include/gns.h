@@ -324,8 +324,8 @@ GNS_API int gns_clip_grads(const gns_tensor* grads, const gns_tensor* outs, int 
  * read, updated and rounded once. step_count (nullable, device): t is read from there (values
  * below 1 count as 1) instead of adamw->step, so that a captured step can be replayed. All
  * roles of a tensor have the same shape; each may have its own ld and stride; they may not
- * alias. A weight that becomes non-finite sets GNS_DEVST_NONFINITE. beta1, beta2 in [0, 1),
- * eps > 0. */
+ * alias. A weight that is stored as a non-finite value sets GNS_DEVST_NONFINITE. beta1, beta2 in
+ * [0, 1), eps > 0; eps, 1 / eps, lr / (1 - beta1) and lr weight_decay finite in fp32. */
 GNS_API int gns_adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, const gns_tensor* V,
                            const gns_tensor* master, int n, const gns_adamw_params* adamw, const float* grad_scale,
                            const int32_t* step_count, int32_t* dev_status, void* stream);

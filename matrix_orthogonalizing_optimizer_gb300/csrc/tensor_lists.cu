@@ -1482,6 +1482,15 @@ int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, co
   if (!(p->beta1 >= 0.0 && p->beta1 < 1.0) || !(p->beta2 >= 0.0 && p->beta2 < 1.0))
     return set_error(GNS_ERR_INVALID, "beta1 and beta2 must be in [0, 1)");
   if (!(p->eps > 0.0) || !std::isfinite(p->eps)) return set_error(GNS_ERR_INVALID, "eps must be finite and > 0");
+  // The kernel's numbers are f32. Where one of these is infinite there, an element whose gradient and
+  // state are zero becomes 0 * inf, a NaN, in place of nothing.
+  const float eps = static_cast<float>(p->eps);
+  if (!std::isfinite(eps) || !std::isfinite(1.f / eps))
+    return set_error(GNS_ERR_INVALID, "eps and 1 / eps must be finite in fp32 (eps above 2^-128)");
+  if (!std::isfinite(static_cast<float>(p->lr / (1.0 - p->beta1))))
+    return set_error(GNS_ERR_INVALID, "lr / (1 - beta1) must be finite in fp32");
+  if (!std::isfinite(static_cast<float>(1.0 - p->lr * p->weight_decay)))
+    return set_error(GNS_ERR_INVALID, "lr weight_decay must be finite in fp32");
   if (!step_count && p->step < 1) return set_error(GNS_ERR_INVALID, "step must be >= 1");
   if (reinterpret_cast<uintptr_t>(grad_scale) % 4 || reinterpret_cast<uintptr_t>(step_count) % 4)
     return set_error(GNS_ERR_INVALID, "grad_scale or step_count: unaligned");
@@ -1512,7 +1521,7 @@ int adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, co
   a.one_minus_beta2 = static_cast<float>(1.0 - p->beta2);
   a.decay = static_cast<float>(1.0 - p->lr * p->weight_decay);
   a.lr = static_cast<float>(p->lr);
-  a.eps = static_cast<float>(p->eps);
+  a.eps = eps;
   const double t = std::max(p->step, 1);
   a.step_size = static_cast<float>(p->lr / (1.0 - std::pow(p->beta1, t)));
   a.rsqrt_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(p->beta2, t)));
