@@ -135,6 +135,21 @@ def _stream_ptr(stream: Optional[torch.cuda.Stream], device) -> int:
     return s.cuda_stream
 
 
+def _on_stream(stream: Optional[torch.cuda.Stream], allocate, returned: bool = False):
+    """What allocate() returns, from the pool of the stream that the call's kernels run on. A block
+    of the current stream's pool may have its last use still queued there, and nothing orders
+    that before another stream's work. returned: the caller gets it, who is on the current
+    stream; its memory then is not used anew before what is queued there when it is freed."""
+    if stream is None:
+        return allocate()
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = allocate()
+    if returned:
+        t.record_stream(caller)
+    return t
+
+
 def _as_list(x) -> List[torch.Tensor]:
     return [x] if isinstance(x, torch.Tensor) else list(x)
 

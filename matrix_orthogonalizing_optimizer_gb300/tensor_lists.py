@@ -22,7 +22,7 @@ import torch
 from . import _lib
 from ._lib import GnsAdamwParams, GnsTensor, load
 from ._lib import check as check_rc
-from .api import _CallStatus, _device_scalar, _dtype_code, _status_ptr, alloc_workspace
+from .api import _CallStatus, _device_scalar, _dtype_code, _on_stream, _status_ptr, alloc_workspace
 
 
 # Field by field a descriptor costs ten times what one packed write does.
@@ -162,15 +162,11 @@ def _norm_buffers(grads: TensorList, result, workspace, stream):
     if grads.has_none:
         raise ValueError("every gradient must be a tensor")
     if result is None:
-        result = torch.empty(2, dtype=torch.float32, device=grads.device)
-        if stream is not None:
-            result.record_stream(stream)
+        result = _on_stream(stream, lambda: torch.empty(2, dtype=torch.float32, device=grads.device), returned=True)
     elif result.dtype != torch.float32 or not result.is_cuda or result.numel() != 2 or not result.is_contiguous():
         raise ValueError("result must be a contiguous CUDA float32 tensor of 2 entries")
     if workspace is None:
-        workspace = alloc_workspace(list_workspace_size(len(grads)), grads.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _on_stream(stream, lambda: alloc_workspace(list_workspace_size(len(grads)), grads.device))
     return result, workspace
 
 
@@ -182,7 +178,8 @@ def grad_norm(grads, max_norm: Optional[float] = None, norm_type: float = 2.0, e
     the gradients to max_norm (1 without max_norm), which adamw_step and muon_step take as
     grad_scale without a pass over the gradients. A norm that is not finite is a device
     condition (see gram_ns_batched): it raises GnsDeviceError unless `status` is given or
-    `check` is off."""
+    `check` is off. With `stream` the call runs there: whoever reads the result on another
+    stream waits for that one first."""
     g = tensor_list(grads)
     code = _norm_code(norm_type)
     result, ws = _norm_buffers(g, result, workspace, stream)

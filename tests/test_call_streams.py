@@ -1,0 +1,147 @@
+"""What a call allocates by itself while it is given a stream: the memory has to come from that stream's
+pool. Memory of the current stream's pool may be a block whose last use is still queued there, which
+nothing orders before the work on the other stream.
+
+On the CPU the allocator, the streams and the library are stand-ins that note what happens; on the GPU the
+current stream is kept busy with writes to memory that it has just freed."""
+import contextlib
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+from matrix_orthogonalizing_optimizer_gb300 import api, tensor_lists  # noqa: E402
+
+
+class _Memory:
+    """A device tensor as far as the calls look at one."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device, stream=None):
+        self.shape = torch.Size((shape,) if isinstance(shape, int) else shape)
+        self.dtype, self.device, self.stream, self.recorded = dtype, device, stream, []
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def element_size(self):
+        return 4
+
+    def stride(self, d=None):
+        s = [math.prod(self.shape[i + 1:]) for i in range(len(self.shape))]
+        return tuple(s) if d is None else s[d]
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+    def __getitem__(self, _):
+        return self
+
+
+class _Stream:
+    def __init__(self, name):
+        self.name, self.cuda_stream, self.device = name, 77, torch.device("cuda", 0)
+
+
+class _Library:
+    """Every entry point: notes nothing and succeeds; sizes are some bytes."""
+
+    def __getattr__(self, name):
+        return lambda *a: 4096 if "size" in name else 0
+
+
+@pytest.fixture
+def world(monkeypatch):
+    here = _Stream("current")
+    now, made = [here], []
+    device = torch.device("cuda", 0)
+
+    @contextlib.contextmanager
+    def stream(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    def empty(*shape, dtype=torch.float32, device=device, **_):
+        shape = shape[0] if len(shape) == 1 else shape
+        made.append(_Memory(shape, dtype, device, now[-1]))
+        return made[-1]
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: now[-1])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: now[-1].cuda_stream, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    for m in (api, tensor_lists):
+        monkeypatch.setattr(m, "load", lambda: _Library())
+    return {"here": here, "made": made, "device": device, "status": _Memory(1, torch.int32, device)}
+
+
+def _tensor(w, *shape, dtype=torch.bfloat16):
+    return _Memory(shape, dtype, w["device"])
+
+
+LIST_CALLS = {
+    "grad_norm": lambda w, **kw: tensor_lists.grad_norm([_tensor(w, 8, 8)], status=w["status"], **kw),
+    "clip_grads": lambda w, **kw: tensor_lists.clip_grads([_tensor(w, 8, 8)], 1.0, status=w["status"], **kw),
+}
+
+
+def _check(world, call):
+    side = _Stream("side")
+    call(world, stream=side)
+    made = [m for m in world["made"] if m.numel()]  # an empty tensor has no memory
+    assert made and all(m.stream is side for m in made)
+    world["made"].clear()
+    call(world)
+    assert all(m.stream is world["here"] for m in world["made"])
+
+
+@pytest.mark.parametrize("name", sorted(LIST_CALLS))
+def test_lists_allocate_on_the_call_s_stream(world, name):
+    _check(world, LIST_CALLS[name])
+
+
+def test_result_is_kept_for_the_stream_that_reads_it(world):
+    """The caller reads the result on the current stream: freed, its memory waits for what is queued there."""
+    r = tensor_lists.grad_norm([_tensor(world, 8, 8)], status=world["status"], stream=_Stream("side"))
+    assert r.recorded == [world["here"]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["grad_norm", "clip_grads"])
+def test_writes_queued_on_the_current_stream_do_not_reach_the_call(call):
+    import matrix_orthogonalizing_optimizer_gb300 as gns
+
+    ts = [torch.full((5000, 100), 0.5, device="cuda") for _ in range(9)]
+    outs = [torch.empty_like(t) for t in ts]
+    want = 0.5 * math.sqrt(9 * 500000)
+    big = torch.empty(1 << 28, dtype=torch.float32, device="cuda")
+    side = torch.cuda.Stream()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    size = gns.list_workspace_size(len(ts))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        freed = [torch.empty(2, device="cuda") for _ in range(64)] + [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(16)]
+        for _ in range(20):
+            big.fill_(1.0)
+        for t in freed:
+            t.fill_(255)
+        freed = t = None
+        if call == "grad_norm":
+            r = gns.grad_norm(ts, max_norm=1.0, stream=side, status=status)
+        else:
+            r = gns.clip_grads(ts, 1.0, outs=outs, stream=side, status=status)
+        torch.cuda.synchronize()
+        assert abs(float(r[0]) - want) <= 2.0 ** -18 * want
+        assert int(status) == 0
