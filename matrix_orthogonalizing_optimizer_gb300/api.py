@@ -267,10 +267,13 @@ def _device_scalar(name: str, t: Optional[torch.Tensor], dtype) -> Optional[int]
 
 def _ns_common(fn_name: str, op: int, xs, outs, ns, workspace, status, stream, check_dev):
     xs = _as_list(xs)
-    outs = [empty_padded(x.shape, x.dtype, x.device) for x in xs] if outs is None else _as_list(outs)
+    if outs is None:
+        outs = [_on_stream(stream, lambda: empty_padded(x.shape, x.dtype, x.device), returned=True) for x in xs]
+    else:
+        outs = _as_list(outs)
     ns = ns or NsParams()
     need = workspace_size(op, xs, ns)
-    ws = workspace if workspace is not None else alloc_workspace(need, xs[0].device)
+    ws = workspace if workspace is not None else _on_stream(stream, lambda: alloc_workspace(need, xs[0].device))
     xa, _ = _batches(xs)
     oa, _ = _batches(outs)
     nsp = ns.c_struct()
@@ -356,7 +359,7 @@ def muon_step(W, G, M, lr: Optional[float] = None, momentum: float = 0.95, weigh
             raise ValueError("muon_step needs lr (or params)")
         params = MuonParams(lr=lr, momentum=momentum, weight_decay=weight_decay, scale=scale, frac=frac)
     need = workspace_size(_lib.GNS_OP_MUON_STEP, Ms, ns, muon=params)
-    ws = workspace if workspace is not None else alloc_workspace(need, Ms[0].device)
+    ws = workspace if workspace is not None else _on_stream(stream, lambda: alloc_workspace(need, Ms[0].device))
     wa, _ = _batches(Ws)
     ga, _ = _batches(Gs)
     ma, _ = _batches(Ms)
@@ -379,11 +382,11 @@ def frac_row_select(m: torch.Tensor, k: int, idx: Optional[torch.Tensor] = None,
     mb = batch_of(m)
     count = mb.count
     if idx is None:
-        idx = torch.empty((count, k), dtype=torch.int32, device=m.device)
+        idx = _on_stream(stream, lambda: torch.empty((count, k), dtype=torch.int32, device=m.device), returned=True)
     if idx.dtype != torch.int32 or not idx.is_contiguous() or idx.numel() < count * k:
         raise ValueError("idx must be a contiguous int32 tensor of count * k entries")
     need = workspace_size(_lib.GNS_OP_FRAC_SELECT, [m])
-    ws = workspace if workspace is not None else alloc_workspace(need, m.device)
+    ws = workspace if workspace is not None else _on_stream(stream, lambda: alloc_workspace(need, m.device))
     gb = batch_of(gathered) if gathered is not None else None
     rc = load().gns_frac_row_select(ctypes.byref(mb), int(k), idx.data_ptr(),
                                     ctypes.byref(gb) if gb is not None else None, ws.data_ptr(), ws.numel(),

@@ -96,6 +96,13 @@ LIST_CALLS = {
     "clip_grads": lambda w, **kw: tensor_lists.clip_grads([_tensor(w, 8, 8)], 1.0, status=w["status"], **kw),
 }
 
+MATRIX_CALLS = {
+    "gram_ns_batched": lambda w, **kw: api.gram_ns_batched([_tensor(w, 2, 8, 16)], status=w["status"], **kw),
+    "ns_standard_batched": lambda w, **kw: api.ns_standard_batched([_tensor(w, 2, 8, 16)], status=w["status"], **kw),
+    "muon_step": lambda w, **kw: api.muon_step(*[[_tensor(w, 2, 8, 16)] for _ in range(3)], lr=0.1, status=w["status"], **kw),
+    "frac_row_select": lambda w, **kw: api.frac_row_select(_tensor(w, 2, 8, 16), 3, **kw),
+}
+
 
 def _check(world, call):
     side = _Stream("side")
@@ -110,6 +117,11 @@ def _check(world, call):
 @pytest.mark.parametrize("name", sorted(LIST_CALLS))
 def test_lists_allocate_on_the_call_s_stream(world, name):
     _check(world, LIST_CALLS[name])
+
+
+@pytest.mark.parametrize("name", sorted(MATRIX_CALLS))
+def test_matrices_allocate_on_the_call_s_stream(world, name):
+    _check(world, MATRIX_CALLS[name])
 
 
 def test_result_is_kept_for_the_stream_that_reads_it(world):
