@@ -209,6 +209,8 @@ def _owned_status(device) -> torch.Tensor:
         if torch.cuda.is_current_stream_capturing():
             raise ValueError("the first call on a device must run outside stream capture (or pass status=)")
         t = torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", idx))
+        # zeroed on the current stream, while the call may be on another one
+        torch.cuda.current_stream(t.device).synchronize()
         _OWNED_STATUS[idx] = t
     return t
 
@@ -217,6 +219,7 @@ def _report(what: str, st: torch.Tensor) -> None:
     v = int(st.cpu()[0])
     if v:
         st.zero_()
+        torch.cuda.current_stream(st.device).synchronize()  # the next call may be on another stream
         raise _lib.GnsDeviceError(what, v)
 
 

@@ -49,7 +49,12 @@ class _Memory:
 
 class _Stream:
     def __init__(self, name):
+        self.waits = 0
         self.name, self.cuda_stream, self.device = name, 77, torch.device("cuda", 0)
+
+
+    def synchronize(self):
+        self.waits += 1
 
 
 class _Library:
@@ -128,6 +133,37 @@ def test_result_is_kept_for_the_stream_that_reads_it(world):
     """The caller reads the result on the current stream: freed, its memory waits for what is queued there."""
     r = tensor_lists.grad_norm([_tensor(world, 8, 8)], status=world["status"], stream=_Stream("side"))
     assert r.recorded == [world["here"]]
+
+
+class _Word(_Memory):
+    """A status word: what is queued on it, and on which stream."""
+    value = 0
+
+    def __getitem__(self, _):
+        return self.value
+
+    def cpu(self):
+        return [self.value]
+
+    def zero_(self):
+        self.value = 0
+
+
+def test_status_word_is_zeroed_before_other_streams_may_set_it(world, monkeypatch):
+    """The module's own status word is zeroed on the current stream; a call on another stream may set its
+    bits as soon as the host goes on."""
+    here, side = world["here"], _Stream("side")
+    monkeypatch.setattr(torch, "zeros", lambda *a, **k: _Word(1, torch.int32, world["device"]))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(api, "_OWNED_STATUS", {})
+    tensor_lists.grad_norm([_tensor(world, 8, 8)], stream=side)
+    assert here.waits == 1  # when the word was made
+    tensor_lists.grad_norm([_tensor(world, 8, 8)], stream=side)
+    assert here.waits == 1
+    api._OWNED_STATUS[0].value = 1
+    with pytest.raises(api._lib.GnsDeviceError):
+        tensor_lists.grad_norm([_tensor(world, 8, 8)], stream=side)
+    assert here.waits == 2 and api._OWNED_STATUS[0].value == 0  # when it was cleared
 
 
 @pytest.mark.gpu
