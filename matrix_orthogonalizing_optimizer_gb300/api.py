@@ -172,11 +172,11 @@ def alloc_workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
-def _status_ptr(status: Optional[torch.Tensor]) -> Optional[int]:
+def _status_ptr(status: Optional[torch.Tensor], index: int) -> Optional[int]:
     if status is None:
         return None
-    if status.dtype != torch.int32 or not status.is_cuda:
-        raise ValueError("status must be a CUDA int32 tensor")
+    if status.dtype != torch.int32 or status.get_device() != index:
+        raise ValueError(f"status must be a CUDA int32 tensor on cuda:{index}")
     return status.data_ptr()
 
 
@@ -236,7 +236,7 @@ class _CallStatus:
         self.device = device
 
     def ptr(self) -> int:
-        return _status_ptr(self.word)
+        return _status_ptr(self.word, _device_index(self.device))
 
     def done(self, what: str) -> None:
         if not self.owned or not self.check or _capturing(self.stream):
@@ -260,11 +260,11 @@ def check_status(status: Optional[torch.Tensor] = None, device=None, what: str =
     _report(what, status)
 
 
-def _device_scalar(name: str, t: Optional[torch.Tensor], dtype) -> Optional[int]:
+def _device_scalar(name: str, t: Optional[torch.Tensor], dtype, index: int) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_cuda or t.numel() != 1:
-        raise ValueError(f"{name} must be a CUDA tensor of one {str(dtype)[6:]}")
+    if t.dtype != dtype or t.get_device() != index or t.numel() != 1:
+        raise ValueError(f"{name} must be a CUDA tensor of one {str(dtype)[6:]} on cuda:{index}")
     return t.data_ptr()
 
 
@@ -373,7 +373,7 @@ def muon_step(W, G, M, lr: Optional[float] = None, momentum: float = 0.95, weigh
     mp = params.c_struct()
     cs = _CallStatus(status, Ms[0].device, check, stream)
     rc = load().gns_muon_step_scaled(wa, ga, ma, va, len(Ms), ctypes.byref(mp), ctypes.byref(nsp),
-                                     _device_scalar("grad_scale", grad_scale, torch.float32), ws.data_ptr(),
+                                     _device_scalar("grad_scale", grad_scale, torch.float32, Ms[0].get_device()), ws.data_ptr(),
                                      ws.numel(), cs.ptr(), _stream_ptr(stream, Ms[0].device))
     check_rc(rc, "gns_muon_step")
     cs.done("gns_muon_step")

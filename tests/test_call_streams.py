@@ -4,96 +4,13 @@ nothing orders before the work on the other stream.
 
 On the CPU the allocator, the streams and the library are stand-ins that note what happens; on the GPU the
 current stream is kept busy with writes to memory that it has just freed."""
-import contextlib
 import math
 
 import pytest
 
 torch = pytest.importorskip("torch")
+from fake_device import Memory, Stream, tensor as _tensor, world  # noqa: E402, F401
 from matrix_orthogonalizing_optimizer_gb300 import api, tensor_lists  # noqa: E402
-
-
-class _Memory:
-    """A device tensor as far as the calls look at one."""
-    is_cuda = True
-
-    def __init__(self, shape, dtype, device, stream=None):
-        self.shape = torch.Size((shape,) if isinstance(shape, int) else shape)
-        self.dtype, self.device, self.stream, self.recorded = dtype, device, stream, []
-
-    def data_ptr(self):
-        return 1 << 20
-
-    def numel(self):
-        return math.prod(self.shape)
-
-    def dim(self):
-        return len(self.shape)
-
-    def is_contiguous(self):
-        return True
-
-    def element_size(self):
-        return 4
-
-    def stride(self, d=None):
-        s = [math.prod(self.shape[i + 1:]) for i in range(len(self.shape))]
-        return tuple(s) if d is None else s[d]
-
-    def record_stream(self, stream):
-        self.recorded.append(stream)
-
-    def __getitem__(self, _):
-        return self
-
-
-class _Stream:
-    def __init__(self, name):
-        self.waits = 0
-        self.name, self.cuda_stream, self.device = name, 77, torch.device("cuda", 0)
-
-
-    def synchronize(self):
-        self.waits += 1
-
-
-class _Library:
-    """Every entry point: notes nothing and succeeds; sizes are some bytes."""
-
-    def __getattr__(self, name):
-        return lambda *a: 4096 if "size" in name else 0
-
-
-@pytest.fixture
-def world(monkeypatch):
-    here = _Stream("current")
-    now, made = [here], []
-    device = torch.device("cuda", 0)
-
-    @contextlib.contextmanager
-    def stream(s):
-        now.append(s)
-        yield
-        now.pop()
-
-    def empty(*shape, dtype=torch.float32, device=device, **_):
-        shape = shape[0] if len(shape) == 1 else shape
-        made.append(_Memory(shape, dtype, device, now[-1]))
-        return made[-1]
-
-    monkeypatch.setattr(torch.cuda, "stream", stream)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: now[-1])
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch, "empty", empty)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: now[-1].cuda_stream, raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
-    for m in (api, tensor_lists):
-        monkeypatch.setattr(m, "load", lambda: _Library())
-    return {"here": here, "made": made, "device": device, "status": _Memory(1, torch.int32, device)}
-
-
-def _tensor(w, *shape, dtype=torch.bfloat16):
-    return _Memory(shape, dtype, w["device"])
 
 
 LIST_CALLS = {
@@ -110,7 +27,7 @@ MATRIX_CALLS = {
 
 
 def _check(world, call):
-    side = _Stream("side")
+    side = Stream("side")
     call(world, stream=side)
     made = [m for m in world["made"] if m.numel()]  # an empty tensor has no memory
     assert made and all(m.stream is side for m in made)
@@ -131,11 +48,11 @@ def test_matrices_allocate_on_the_call_s_stream(world, name):
 
 def test_result_is_kept_for_the_stream_that_reads_it(world):
     """The caller reads the result on the current stream: freed, its memory waits for what is queued there."""
-    r = tensor_lists.grad_norm([_tensor(world, 8, 8)], status=world["status"], stream=_Stream("side"))
+    r = tensor_lists.grad_norm([_tensor(world, 8, 8)], status=world["status"], stream=Stream("side"))
     assert r.recorded == [world["here"]]
 
 
-class _Word(_Memory):
+class _Word(Memory):
     """A status word: what is queued on it, and on which stream."""
     value = 0
 
@@ -152,7 +69,7 @@ class _Word(_Memory):
 def test_status_word_is_zeroed_before_other_streams_may_set_it(world, monkeypatch):
     """The module's own status word is zeroed on the current stream; a call on another stream may set its
     bits as soon as the host goes on."""
-    here, side = world["here"], _Stream("side")
+    here, side = world["here"], Stream("side")
     monkeypatch.setattr(torch, "zeros", lambda *a, **k: _Word(1, torch.int32, world["device"]))
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(api, "_OWNED_STATUS", {})
