@@ -130,8 +130,31 @@ def _batches(ts: Iterable[torch.Tensor]):
     return arr, ts
 
 
+def _elsewhere(name: str, index: int) -> ValueError:
+    return ValueError(f"{name} must be on the device of the tensors, cuda:{index}")
+
+
+def _one_device(index: int, **tensors) -> None:
+    """Raises unless each of the named tensors (or lists of them, or None) is on device `index`."""
+    for name, ts in tensors.items():
+        for t in _as_list(ts) if ts is not None else ():
+            if t.get_device() != index:
+                raise _elsewhere(name, index)
+
+
+def _launch(index: int, entry, *args) -> int:
+    """entry(*args) with the tensors' device as the current one: a stream's handle of 0 is the
+    current device's default stream."""
+    if torch.cuda.device_count() == 1 or torch.cuda.current_device() == index:
+        return entry(*args)
+    with torch.cuda.device(index):
+        return entry(*args)
+
+
 def _stream_ptr(stream: Optional[torch.cuda.Stream], device) -> int:
     s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device.index != device.index:
+        raise _elsewhere("stream", device.index)
     return s.cuda_stream
 
 
@@ -279,11 +302,13 @@ def _ns_common(fn_name: str, op: int, xs, outs, ns, workspace, status, stream, c
     ws = workspace if workspace is not None else _on_stream(stream, lambda: alloc_workspace(need, xs[0].device))
     xa, _ = _batches(xs)
     oa, _ = _batches(outs)
+    device = xs[0].device
+    _one_device(device.index, xs=xs, outs=outs, workspace=ws)
     nsp = ns.c_struct()
     fn = getattr(load(), fn_name)
-    cs = _CallStatus(status, xs[0].device, check_dev, stream)
-    rc = fn(xa, oa, len(xs), _dtype_code(xs[0]), ctypes.byref(nsp), ws.data_ptr(), ws.numel(),
-            cs.ptr(), _stream_ptr(stream, xs[0].device))
+    cs = _CallStatus(status, device, check_dev, stream)
+    rc = _launch(device.index, fn, xa, oa, len(xs), _dtype_code(xs[0]), ctypes.byref(nsp), ws.data_ptr(), ws.numel(),
+                 cs.ptr(), _stream_ptr(stream, device))
     check_rc(rc, fn_name)
     cs.done(fn_name)
     return outs
@@ -313,9 +338,10 @@ def ns_standard_batched(xs, outs=None, ns: Optional[NsParams] = None, workspace=
 def sym_gemm_xxt(x: torch.Tensor, c: torch.Tensor, alpha: float = 1.0, beta: float = 0.0, status=None, stream=None,
                  check: bool = True):
     xb, cb = batch_of(x), batch_of(c)
+    _one_device(x.device.index, c=c)
     cs = _CallStatus(status, x.device, check, stream)
-    rc = load().gns_sym_gemm_xxt(ctypes.byref(xb), ctypes.byref(cb), float(alpha), float(beta), _dtype_code(x),
-                                 cs.ptr(), _stream_ptr(stream, x.device))
+    rc = _launch(x.device.index, load().gns_sym_gemm_xxt, ctypes.byref(xb), ctypes.byref(cb), float(alpha), float(beta),
+                 _dtype_code(x), cs.ptr(), _stream_ptr(stream, x.device))
     check_rc(rc, "gns_sym_gemm_xxt")
     cs.done("gns_sym_gemm_xxt")
     return c
@@ -325,10 +351,11 @@ def sym_gemm(a: torch.Tensor, b: torch.Tensor, c: Optional[torch.Tensor], d: tor
              beta: float = 0.0, status=None, stream=None, check: bool = True):
     ab, bb, db = batch_of(a), batch_of(b), batch_of(d)
     cb = batch_of(c) if c is not None else None
+    _one_device(a.device.index, b=b, c=c, d=d)
     cs = _CallStatus(status, a.device, check, stream)
-    rc = load().gns_sym_gemm(ctypes.byref(ab), ctypes.byref(bb), ctypes.byref(cb) if cb is not None else None,
-                             ctypes.byref(db), float(alpha), float(beta), _dtype_code(a), cs.ptr(),
-                             _stream_ptr(stream, a.device))
+    rc = _launch(a.device.index, load().gns_sym_gemm, ctypes.byref(ab), ctypes.byref(bb),
+                 ctypes.byref(cb) if cb is not None else None, ctypes.byref(db), float(alpha), float(beta),
+                 _dtype_code(a), cs.ptr(), _stream_ptr(stream, a.device))
     check_rc(rc, "gns_sym_gemm")
     cs.done("gns_sym_gemm")
     return d
@@ -338,10 +365,11 @@ def sym_poly_update(R, Q, Z, RZ, q_scratch, a: float, b: float, c: float, q_is_i
                     status=None, stream=None, check: bool = True):
     bs = [batch_of(t) for t in (R, Q, Z, RZ)]
     qs = batch_of(q_scratch) if q_scratch is not None else None
+    _one_device(R.device.index, Q=Q, Z=Z, RZ=RZ, q_scratch=q_scratch)
     cs = _CallStatus(status, R.device, check, stream)
-    rc = load().gns_sym_poly_update(*[ctypes.byref(x) for x in bs], ctypes.byref(qs) if qs is not None else None,
-                                    float(a), float(b), float(c), int(bool(q_is_identity)), int(bool(skip_r)),
-                                    _dtype_code(R), cs.ptr(), _stream_ptr(stream, R.device))
+    rc = _launch(R.device.index, load().gns_sym_poly_update, *[ctypes.byref(x) for x in bs],
+                 ctypes.byref(qs) if qs is not None else None, float(a), float(b), float(c), int(bool(q_is_identity)),
+                 int(bool(skip_r)), _dtype_code(R), cs.ptr(), _stream_ptr(stream, R.device))
     check_rc(rc, "gns_sym_poly_update")
     cs.done("gns_sym_poly_update")
 
@@ -371,10 +399,12 @@ def muon_step(W, G, M, lr: Optional[float] = None, momentum: float = 0.95, weigh
         va, _ = _batches(_as_list(V))
     nsp = ns.c_struct()
     mp = params.c_struct()
-    cs = _CallStatus(status, Ms[0].device, check, stream)
-    rc = load().gns_muon_step_scaled(wa, ga, ma, va, len(Ms), ctypes.byref(mp), ctypes.byref(nsp),
-                                     _device_scalar("grad_scale", grad_scale, torch.float32, Ms[0].get_device()), ws.data_ptr(),
-                                     ws.numel(), cs.ptr(), _stream_ptr(stream, Ms[0].device))
+    device = Ms[0].device
+    _one_device(device.index, W=Ws, G=Gs, M=Ms, V=V, workspace=ws)
+    cs = _CallStatus(status, device, check, stream)
+    rc = _launch(device.index, load().gns_muon_step_scaled, wa, ga, ma, va, len(Ms), ctypes.byref(mp), ctypes.byref(nsp),
+                 _device_scalar("grad_scale", grad_scale, torch.float32, device.index), ws.data_ptr(), ws.numel(),
+                 cs.ptr(), _stream_ptr(stream, device))
     check_rc(rc, "gns_muon_step")
     cs.done("gns_muon_step")
 
@@ -391,9 +421,10 @@ def frac_row_select(m: torch.Tensor, k: int, idx: Optional[torch.Tensor] = None,
     need = workspace_size(_lib.GNS_OP_FRAC_SELECT, [m])
     ws = workspace if workspace is not None else _on_stream(stream, lambda: alloc_workspace(need, m.device))
     gb = batch_of(gathered) if gathered is not None else None
-    rc = load().gns_frac_row_select(ctypes.byref(mb), int(k), idx.data_ptr(),
-                                    ctypes.byref(gb) if gb is not None else None, ws.data_ptr(), ws.numel(),
-                                    _stream_ptr(stream, m.device))
+    _one_device(m.device.index, idx=idx, gathered=gathered, workspace=ws)
+    rc = _launch(m.device.index, load().gns_frac_row_select, ctypes.byref(mb), int(k), idx.data_ptr(),
+                 ctypes.byref(gb) if gb is not None else None, ws.data_ptr(), ws.numel(),
+                 _stream_ptr(stream, m.device))
     check_rc(rc, "gns_frac_row_select")
     return idx
 

@@ -22,7 +22,7 @@ import torch
 from . import _lib
 from ._lib import GnsAdamwParams, GnsTensor, load
 from ._lib import check as check_rc
-from .api import _CallStatus, _device_scalar, _dtype_code, _on_stream, _status_ptr, alloc_workspace
+from .api import _CallStatus, _device_scalar, _dtype_code, _elsewhere, _on_stream, _status_ptr, alloc_workspace
 
 
 # Field by field a descriptor costs ten times what one packed write does.
@@ -136,10 +136,6 @@ def _stream(stream: Optional[torch.cuda.Stream], index: int) -> int:
     if stream.device.index != index:
         raise _elsewhere("stream", index)
     return stream.cuda_stream
-
-
-def _elsewhere(name: str, index: int) -> ValueError:
-    return ValueError(f"{name} must be on the device of the tensors, cuda:{index}")
 
 
 def _device_of(x: TensorList):

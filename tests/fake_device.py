@@ -91,8 +91,14 @@ def world(monkeypatch):
         made.append(Memory(shape, dtype, device, now[-1]))
         return made[-1]
 
+    def current_stream(d=None):
+        index = 0 if d is None else torch.device(d).index
+        return now[-1] if now[-1].device.index == index else Stream("another device's", index)
+
     monkeypatch.setattr(torch.cuda, "stream", stream)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: now[-1])
+    monkeypatch.setattr(torch.cuda, "current_stream", current_stream)
+    # a tensor is one tensor, not a list of its rows
+    monkeypatch.setattr(api, "_as_list", lambda x: [x] if isinstance(x, Memory) else list(x))
     monkeypatch.setattr(torch.cuda, "device", on_device)
     monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: devices[-1])

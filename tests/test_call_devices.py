@@ -5,7 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 from fake_device import Memory, Stream, tensor, world  # noqa: E402, F401
-from matrix_orthogonalizing_optimizer_gb300 import tensor_lists  # noqa: E402
+from matrix_orthogonalizing_optimizer_gb300 import api, tensor_lists  # noqa: E402
 
 F32, I32, U8 = torch.float32, torch.int32, torch.uint8
 
@@ -80,3 +80,79 @@ def test_lists_of_no_tensor_are_refused(world):
                  lambda: tensor_lists.adamw_step([None], [None], [None], [None], lr=0.1)):
         with pytest.raises(ValueError, match="must be a tensor"):
             call()
+
+
+def _matrix(index, *shape):
+    return [_memory(shape or (2, 8, 16), torch.bfloat16, index)]
+
+
+def _gram(w, index, **kw):
+    api.gram_ns_batched(**{"xs": _matrix(index), "status": _memory(1, I32, index), **kw})
+
+
+def _standard(w, index, **kw):
+    api.ns_standard_batched(**{"xs": _matrix(index), "status": _memory(1, I32, index), **kw})
+
+
+def _muon(w, index, **kw):
+    roles = {k: _matrix(index) for k in "WGM"}
+    api.muon_step(**{**roles, "lr": 0.1, "status": _memory(1, I32, index), **kw})
+
+
+def _select(w, index, **kw):
+    api.frac_row_select(**{"m": _matrix(index)[0], "k": 3, **kw})
+
+
+def _gemm(w, index, **kw):
+    roles = {k: _matrix(index)[0] for k in "abcd"}
+    api.sym_gemm(**{**roles, "status": _memory(1, I32, index), **kw})
+
+
+def _xxt(w, index, **kw):
+    api.sym_gemm_xxt(**{"x": _matrix(index)[0], "c": _matrix(index)[0], "status": _memory(1, I32, index), **kw})
+
+
+def _poly(w, index, **kw):
+    roles = {k: _matrix(index)[0] for k in ("R", "Q", "Z", "RZ", "q_scratch")}
+    api.sym_poly_update(**{**roles, "a": 1.0, "b": 1.0, "c": 1.0, "q_is_identity": False, "skip_r": False,
+                           "status": _memory(1, I32, index), **kw})
+
+
+def _one(index):
+    return _matrix(index)[0]
+
+
+STATUS, STREAM = lambda i: _memory(1, I32, i), lambda i: Stream("side", i)  # noqa: E731
+WORKSPACE = lambda i: _memory(1 << 20, U8, i)  # noqa: E731
+MATRICES = {
+    _gram: dict(outs=_matrix, workspace=WORKSPACE, status=STATUS, stream=STREAM),
+    _standard: dict(outs=_matrix, workspace=WORKSPACE, status=STATUS, stream=STREAM),
+    _muon: dict(W=_matrix, G=_matrix, V=lambda i: [_memory((2, 1, 8), F32, i)], workspace=WORKSPACE, status=STATUS,
+                stream=STREAM, grad_scale=lambda i: _memory(1, F32, i)),
+    _select: dict(idx=lambda i: _memory((2, 3), I32, i), gathered=_one, workspace=WORKSPACE, stream=STREAM),
+    _gemm: dict(b=_one, c=_one, d=_one, status=STATUS, stream=STREAM),
+    _xxt: dict(c=_one, status=STATUS, stream=STREAM),
+    _poly: dict(Q=_one, Z=_one, RZ=_one, q_scratch=_one, status=STATUS, stream=STREAM),
+}
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, names in MATRICES.items() for n in names])
+def test_matrices_refuse_what_lies_on_another_device(world, call, name):
+    make = MATRICES[call][name]
+    call(world, 0, **{name: make(0)})
+    assert len(world["library"].calls) == 1
+    with pytest.raises(ValueError, match=name):
+        call(world, 0, **{name: make(1)})
+    assert len(world["library"].calls) == 1
+
+
+def test_groups_of_one_call_lie_on_one_device(world):
+    with pytest.raises(ValueError, match="xs"):
+        _gram(world, 0, xs=_matrix(0) + _matrix(1))
+
+
+@pytest.mark.parametrize("call", list(MATRICES))
+@pytest.mark.parametrize("index", [0, 1])
+def test_matrices_launch_on_the_device_of_their_tensors(world, call, index):
+    call(world, index)
+    assert [i for _, i in world["library"].calls] == [index]
