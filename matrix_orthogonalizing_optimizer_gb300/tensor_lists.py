@@ -15,6 +15,7 @@ import ctypes
 import math
 import struct
 from dataclasses import dataclass
+from functools import cached_property
 from typing import Optional, Sequence, Union
 
 import torch
@@ -117,6 +118,10 @@ class TensorList:
         self.layout_key = hash((self.index, *layout))
         self.reordered = any(x is not None and x and type(x[0]) is tuple for x in layout)
 
+    @cached_property
+    def has_empty(self) -> bool:
+        return any(x and 0 in x for x in self.layout)
+
     def __len__(self):
         return len(self.tensors)
 
@@ -151,8 +156,10 @@ def _same_layout(name: str, a: TensorList, b: TensorList, optional: bool = False
         return
     if a.index != b.index and b.index is not None:
         raise _elsewhere(name, a.index)
-    if optional and not a.reordered and not b.reordered and len(a) == len(b):
-        return  # the library compares the shapes itself: what it cannot see is the order in memory
+    if optional and not a.reordered and not b.reordered and not b.has_empty and len(a) == len(b):
+        # the library compares the shapes itself: what it cannot see is the order in memory, and an empty
+        # tensor where it takes one for none
+        return
     if len(a) != len(b):
         raise ValueError(f"{name}: {len(b)} tensors, expected {len(a)}")
     for i, (x, y) in enumerate(zip(a.layout, b.layout)):
