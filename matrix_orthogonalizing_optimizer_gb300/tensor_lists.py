@@ -62,23 +62,25 @@ def _describe(array, at: int, t: torch.Tensor):
     if n == 3 and steps[2] == 1 and steps[1] >= shape[2] and steps[0] >= (shape[1] - 1) * steps[1] + shape[2]:
         _PACK(array, at, t.data_ptr(), *shape, steps[1], steps[0], code, 0)
         return shape
-    order = tuple(sorted(range(n), key=lambda d: (-t.stride(d), -shape[d], d)))
-    u = t.permute(order)
-    if u.is_contiguous():
-        _describe(array, at, u)
+    # a dimension of size 1 has a stride of no meaning
+    dims = [d for d in range(n) if shape[d] != 1]
+    order = tuple(sorted(dims, key=lambda d: (-steps[d], -shape[d], d)))
+    whole = 1
+    for d in reversed(order):
+        if steps[d] != whole:
+            break
+        whole *= shape[d]
+    else:  # a permutation of a contiguous tensor: the one that it permutes
+        count, rows, cols = math.prod([shape[d] for d in order[:-2]]), shape[order[-2]], shape[order[-1]]
+        _PACK(array, at, t.data_ptr(), count, rows, cols, cols, rows * cols, code, 0)
         return shape, order
     # leading dimensions that lie evenly behind one another are one
-    dims, steps = list(shape), list(steps)
-    while len(dims) > 3 and (dims[0] == 1 or steps[0] == steps[1] * dims[1]):
-        d0 = dims.pop(0)
-        steps.pop(0)
-        dims[0] *= d0
-    while len(dims) < 3:
-        dims.insert(0, 1)
-        steps.insert(0, 0)
-    (count, rows, cols), (stride, ld, one) = dims[-3:], steps[-3:]
-    if len(dims) > 3 or (one != 1 and cols > 1) or (rows > 1 and ld < cols) or (
-            count > 1 and stride < (rows - 1) * ld * (rows > 1) + cols):
+    rows, ld = (shape[-2], steps[-2]) if n > 1 else (1, 0)
+    cols, one = shape[-1], steps[-1]
+    lead = [d for d in dims if d < n - 2]
+    count, stride = math.prod([shape[d] for d in lead]), steps[lead[-1]] if lead else 0
+    if any(steps[a] != steps[b] * shape[b] for a, b in zip(lead, lead[1:])) or (one != 1 and cols > 1) or (
+            rows > 1 and ld < cols) or (count > 1 and stride < (rows - 1) * ld * (rows > 1) + cols):
         raise ValueError(f"a tensor of shape {shape} with strides {tuple(t.stride())} is neither without gaps nor a "
                          "batch of rows with a contiguous last dimension: make it contiguous")
     _PACK(array, at, t.data_ptr(), count, rows, cols, max(ld, cols), stride, code, 0)

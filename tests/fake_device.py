@@ -112,3 +112,30 @@ def world(monkeypatch):
 
 def tensor(w, *shape, dtype=torch.bfloat16, index=0):
     return Memory(shape, dtype, torch.device("cuda", index))
+
+
+class OnDevice:
+    """A CPU tensor that says it lives on a GPU: describing it launches nothing."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    dtype = property(lambda s: s.t.dtype)
+    shape = property(lambda s: s.t.shape)
+    device = property(lambda s: s.t.device)
+
+    def data_ptr(self):
+        return self.t.data_ptr()
+
+    def numel(self):
+        return self.t.numel()
+
+    def stride(self, d=None):
+        return self.t.stride() if d is None else self.t.stride(d)
+
+    def is_contiguous(self):
+        return self.t.is_contiguous()
+
+    def permute(self, order):
+        return OnDevice(self.t.permute(order))
