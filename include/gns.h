@@ -302,9 +302,10 @@ GNS_API size_t gns_list_workspace_size(int n);
  * result: two device floats. Sums are formed in a fixed order (the same bits for the same
  * list and sizes), squares never overflow or vanish: N is right over the whole range of the
  * types. The call's last block gathers what the others have summed; should it have to wait for
- * them beyond the library's limit, N is NaN and GNS_DEVST_TIMEOUT is set. A NaN gradient gives N = NaN and a NaN scale, an infinite one N = inf and scale 0;
- * either sets GNS_DEVST_NONFINITE. A list of empty tensors has N = 0. max_norm >= 0 and not
- * NaN, eps >= 0 and finite. */
+ * them beyond the library's limit, N is NaN and GNS_DEVST_TIMEOUT is set. A NaN gradient gives
+ * N = NaN and a NaN scale, an infinite one N = inf and scale 0, unless max_norm is infinity: the
+ * scale is then 1 whatever N is. Either sets GNS_DEVST_NONFINITE. A list of empty tensors has
+ * N = 0. max_norm >= 0 and not NaN, eps >= 0 and finite. */
 GNS_API int gns_grad_norm(const gns_tensor* grads, int n, int norm_type, float max_norm, float eps, float* result,
                           void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 

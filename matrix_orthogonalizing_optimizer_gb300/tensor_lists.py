@@ -207,8 +207,8 @@ def grad_norm(grads, max_norm: Optional[float] = None, norm_type: float = 2.0, e
     """Global norm of a list of gradients: the square root of the sum of squares over all of
     them (norm_type 2), or their largest magnitude (math.inf). Returns `result`, a float32
     tensor: result[0] the norm, result[1] the scale min(1, max_norm / (norm + eps)) that clips
-    the gradients to max_norm (1 without max_norm), which adamw_step and muon_step take as
-    grad_scale without a pass over the gradients. A norm that is not finite is a device
+    the gradients to max_norm (1 without max_norm, also where the norm is not finite), which
+    adamw_step and muon_step take as grad_scale without a pass over the gradients. A norm that is not finite is a device
     condition (see gram_ns_batched): it raises GnsDeviceError unless `status` is given or
     `check` is off. With `stream` the call runs there: whoever reads the result on another
     stream waits for that one first."""
