@@ -344,6 +344,18 @@ GNS_API int gns_adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_t
 GNS_API int gns_selftest_bounded_wait(const int32_t* counter, int32_t target, uint32_t limit_us,
                                       int32_t* dev_status, uint64_t* out, void* stream);
 
+/* Self-test of the wait in gns_grad_norm (no GPU fault is involved): the same gathering of the
+ * blocks' shares, alone, over nslots slots in ws with a limit of limit_us, and the same handing in
+ * of shares (1 each), all with one call's number as a replayed graph has it. Enqueued: the first
+ * `early` shares are handed in; gathering (result[0..1]); `late` further ones, as by blocks that
+ * the gathering no longer waited for; gathering again (result[2..3]), which may not take these;
+ * every share, late ones first, then the next replay's; gathering (result[4..5]). Where early <
+ * nslots the first norm is NaN and GNS_DEVST_TIMEOUT is set, as with the second in any case; the
+ * third is sqrt(nslots), or 1 (norm_type). out (nullable, device, three uint64): the nanoseconds
+ * of each gathering. result: six device floats; ws: 256-byte aligned, nslots 16-byte slots. */
+GNS_API int gns_selftest_norm_wait(void* ws, size_t ws_bytes, int nslots, int early, int late, int norm_type,
+                                   uint32_t limit_us, float* result, uint64_t* out, int32_t* dev_status, void* stream);
+
 /* Size of the fixed scratch array behind gns_gram_ns_batched_noalloc (64 MiB). */
 #define GNS_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
 

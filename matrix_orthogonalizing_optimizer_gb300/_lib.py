@@ -35,7 +35,7 @@ EXPORTS = [
     "gns_version", "gns_status_string", "gns_last_error", "gns_ns_params_default", "gns_workspace_size",
     "gns_gram_ns_batched", "gns_ns_standard_batched", "gns_sym_gemm_xxt", "gns_sym_gemm",
     "gns_sym_poly_update", "gns_muon_step", "gns_frac_row_select", "gns_profile_set", "gns_profile_query", "gns_gram_ns_batched_noalloc",
-    "gns_selftest_bounded_wait",
+    "gns_selftest_bounded_wait", "gns_selftest_norm_wait",
     "gns_muon_step_scaled", "gns_list_workspace_size", "gns_grad_norm", "gns_clip_grads", "gns_adamw_step",
 ]
 
@@ -136,6 +136,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gns_adamw_step.argtypes = [vp, vp, vp, vp, vp, i32, P(GnsAdamwParams), vp, vp, vp, vp]
     lib.gns_selftest_bounded_wait.restype = i32
     lib.gns_selftest_bounded_wait.argtypes = [vp, i32, ctypes.c_uint32, vp, vp, vp]
+    lib.gns_selftest_norm_wait.restype = i32
+    lib.gns_selftest_norm_wait.argtypes = [vp, sz, i32, i32, i32, i32, ctypes.c_uint32, vp, vp, vp, vp]
     lib.gns_profile_set.restype = i32
     lib.gns_profile_set.argtypes = [P(vp), i32]
     lib.gns_profile_query.restype = i32

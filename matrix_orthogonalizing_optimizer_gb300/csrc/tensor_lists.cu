@@ -620,6 +620,29 @@ GNS_DEV Slot get_slot(const Slot* s) {
   return r;
 }
 
+// Writes a slot and returns what was there, as one access.
+GNS_DEV Slot exchange_slot(Slot* s, Share v, unsigned long long call) {
+  uint32_t m;
+  Slot r;
+  asm volatile(
+      "{\n\t.reg .b128 x, y;\n\t.reg .b64 v;\n\tmov.b64 v, {%4, %5};\n\tmov.b128 x, {v, %6};\n\t"
+      "atom.relaxed.gpu.global.exch.b128 y, [%3], x;\n\tmov.b128 {v, %2}, y;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "=r"(m), "=r"(r.share.e), "=l"(r.call)
+      : "l"(s), "r"(__float_as_uint(v.m)), "r"(v.e), "l"(call)
+      : "memory");
+  r.share.m = __uint_as_float(m);
+  return r;
+}
+
+// Who gathers the shares and no longer waits for a slot's closes it, by this number in the call's place.
+GNS_DEV unsigned long long closed(unsigned long long call) { return ~call; }
+
+// Hands in a share that is waited for. Where its slot has been closed the share stays behind, and the
+// slot is cleared: a replay of the captured call has the same number, and would take it for its own.
+GNS_DEV void hand_in(Slot* s, Share v, unsigned long long call) {
+  if (exchange_slot(s, v, call).call == closed(call)) put_slot(s, {0.f, 0}, 0);
+}
+
 // What a norm call leaves in result[0] and result[1], from the slots of its launches.
 struct Finish {
   Slot* slots;
@@ -630,6 +653,7 @@ struct Finish {
   int inf;
   float max_norm;  // infinity: no clipping
   float eps;
+  unsigned long long limit_ns = GNS_WAIT_TIMEOUT_NS;  // of the wait for the slots
 };
 
 // Shares are added as they are where all have e = 0, which nearly always they do. Otherwise the
@@ -650,24 +674,31 @@ GNS_DEV void norm_and_scale(const Finish& f, float n, int e, float* norm, float*
 }
 
 // The norm and the scale, in every thread of the block, from slots that hold this call's shares
-// (WAIT = false) or will do so (WAIT = true), added in a fixed order. Waiting ends after
-// GNS_WAIT_TIMEOUT_NS at the latest, with a NaN and the timeout bit.
+// (WAIT = false) or will do so (WAIT = true), added in a fixed order. Waiting ends after limit_ns
+// at the latest, however many slots are still open: these are closed, the norm is NaN and the
+// timeout bit is set.
 template <bool WAIT>
 GNS_DEV void finish_norm(const Finish& f, float* norm, float* scale) {
   uint32_t most = 0, seen = 0;
   float n = 0.f;
+  uint64_t t0 = 0;
+  bool late = false;  // this thread has closed a slot
   for (int i = threadIdx.x; i < f.nslots; i += THREADS) {
     Slot s = get_slot(f.slots + i);
     if (WAIT) {
-      uint64_t t0 = 0;
       for (uint32_t k = 1; s.call != f.call; ++k) {
-        if ((k & 63u) == 0u) {
+        if (late || (k & 63u) == 0u) {
           const uint64_t now = global_timer_ns();
           if (!t0) t0 = now;
-          if (now - t0 > GNS_WAIT_TIMEOUT_NS) {
-            set_status(f.status, GNS_DEVST_TIMEOUT);
-            s.share = {__int_as_float(0x7fffffff), 0};
-            put_slot(f.slots + i, s.share, f.call);
+          if (late || now - t0 > f.limit_ns) {
+            const Share none = {__int_as_float(0x7fffffff), 0};
+            s = exchange_slot(f.slots + i, none, closed(f.call));
+            if (s.call != f.call) {
+              s.share = none;
+              late = true;
+            } else {  // handed in meanwhile
+              put_slot(f.slots + i, s.share, f.call);
+            }
             break;
           }
         }
@@ -678,6 +709,7 @@ GNS_DEV void finish_norm(const Finish& f, float* norm, float* scale) {
     n += s.share.m;
     seen |= exponents(s.share);
   }
+  if (WAIT && late) set_status(f.status, GNS_DEVST_TIMEOUT);
   int top = 0;
   if (f.inf) {
     n = __uint_as_float(block_max<THREADS>(most));
@@ -686,12 +718,14 @@ GNS_DEV void finish_norm(const Finish& f, float* norm, float* scale) {
     top = top_exponent(seen);
     n = 0.f;
     for (int i = threadIdx.x; i < f.nslots; i += THREADS) n += scaled_share(get_slot(f.slots + i).share, top);
+    if (WAIT && late) n = __int_as_float(0x7fffffff);  // what a closed slot holds now counts for nothing
     n = block_sum<THREADS>(n);
   } else {
     n = block_sum<THREADS>(n);
   }
-  if (WAIT)  // a replay of the captured call writes the same number again
-    for (int i = threadIdx.x; i < f.nslots; i += THREADS) put_slot(f.slots + i, {0.f, 0}, 0);
+  if (WAIT)  // a replay of the captured call writes the same number again; a closed slot's block clears it
+    for (int i = threadIdx.x; i < f.nslots; i += THREADS)
+      if (!late || get_slot(f.slots + i).call != closed(f.call)) put_slot(f.slots + i, {0.f, 0}, 0);
   norm_and_scale(f, n, top, norm, scale);
 }
 
@@ -719,12 +753,29 @@ __global__ void __launch_bounds__(THREADS, NORM_BLOCKS) norm_kernel(const __grid
     uint32_t bits = 0;
     s = square_share<THREADS>([&](float pre, auto scaled) { return sum_squares<scaled.value>(l, pre, &bits); }, bits);
   }
-  if (threadIdx.x == 0) put_slot(slots + blockIdx.x, s, f.call);
+  if (threadIdx.x == 0) {
+    if (finish)
+      hand_in(slots + blockIdx.x, s, f.call);
+    else  // the launch that gathers begins when this one has ended
+      put_slot(slots + blockIdx.x, s, f.call);
+  }
   if (finish && blockIdx.x == gridDim.x - 1) {
     float norm, scale;
     finish_norm<true>(f, &norm, &scale);
     write_result(f, norm, scale);
   }
+}
+
+// Self-test of the wait: the gathering alone, timed, and the handing in of shares of 1 alone.
+__global__ void __launch_bounds__(THREADS) selftest_gather_kernel(Finish f, unsigned long long* out) {
+  const uint64_t t0 = global_timer_ns();
+  float norm, scale;
+  finish_norm<true>(f, &norm, &scale);
+  write_result(f, norm, scale);
+  if (out && threadIdx.x == 0) *out = global_timer_ns() - t0;
+}
+__global__ void __launch_bounds__(THREADS) selftest_hand_in_kernel(Slot* slots, int n, unsigned long long call) {
+  for (int i = threadIdx.x; i < n; i += THREADS) hand_in(slots + i, {1.f, 0}, call);
 }
 
 // A list of empty tensors.
@@ -1433,6 +1484,35 @@ int grad_norm(const gns_tensor* g, int n, int norm_type, float max_norm, float e
   return norm_launches(g, n, left, stream, true, &f);
 }
 
+int selftest_norm_wait(void* ws, size_t ws_bytes, int nslots, int early, int late, int norm_type, uint32_t limit_us,
+                       float* result, unsigned long long* out, int32_t* dev_status, void* stream) {
+  if (!ws || !result) return set_error(GNS_ERR_INVALID, "null argument");
+  if (reinterpret_cast<uintptr_t>(result) % 4 || reinterpret_cast<uintptr_t>(out) % 8)
+    return set_error(GNS_ERR_INVALID, "result or out: unaligned");
+  if (nslots < 1 || nslots > 1 << 16 || early < 0 || late < 0 || early + late > nslots)
+    return set_error(GNS_ERR_INVALID, "nslots must be in [1, 65536] and hold early + late");
+  if (norm_type != GNS_NORM_L2 && norm_type != GNS_NORM_INF) return set_error(GNS_ERR_INVALID, "unknown norm type");
+  if (limit_us < 1 || limit_us > 1000000) return set_error(GNS_ERR_INVALID, "limit_us must be in [1, 1000000]");
+  if (reinterpret_cast<uintptr_t>(ws) % 256 || ws_bytes < nslots * sizeof(Slot))
+    return set_error(GNS_ERR_WORKSPACE, "workspace unaligned or too small");
+  Slot* const slots = static_cast<Slot*>(ws);
+  Finish f = {slots,     call_number(), result, dev_status, nslots, norm_type == GNS_NORM_INF,
+              INFINITY, 0.f,           limit_us * 1000ull};
+  auto hand = [&](Slot* at, int n) {
+    return launch("norm self-test", selftest_hand_in_kernel, 1, THREADS, stream, ALONE, at, n, f.call);
+  };
+  auto gather = [&](int k) {
+    f.result = result + 2 * k;
+    unsigned long long* const time = out ? out + k : nullptr;
+    return launch("norm self-test", selftest_gather_kernel, 1, THREADS, stream, ALONE, f, time);
+  };
+  int rc;
+  if ((rc = hand(slots, early)) || (rc = gather(0)) || (rc = hand(slots + early, late)) || (rc = gather(1)) ||
+      (rc = hand(slots, nslots)) || (rc = hand(slots, nslots)))
+    return rc;
+  return gather(2);
+}
+
 int clip_grads(const gns_tensor* g, const gns_tensor* out, int n, int norm_type, float max_norm, float eps,
                float* result, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
   if (int rc = check_norm(g, n, norm_type, max_norm, eps, result, ws, ws_bytes)) return rc;
@@ -1574,6 +1654,14 @@ GNS_API int gns_grad_norm(const gns_tensor* grads, int n, int norm_type, float m
                           void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
   return guarded(
       [&] { return grad_norm(grads, n, norm_type, max_norm, eps, result, ws, ws_bytes, dev_status, stream); });
+}
+
+GNS_API int gns_selftest_norm_wait(void* ws, size_t ws_bytes, int nslots, int early, int late, int norm_type,
+                                   uint32_t limit_us, float* result, uint64_t* out, int32_t* dev_status, void* stream) {
+  return guarded([&] {
+    return selftest_norm_wait(ws, ws_bytes, nslots, early, late, norm_type, limit_us, result,
+                              reinterpret_cast<unsigned long long*>(out), dev_status, stream);
+  });
 }
 
 GNS_API int gns_clip_grads(const gns_tensor* grads, const gns_tensor* outs, int n, int norm_type, float max_norm,
