@@ -1318,9 +1318,8 @@ int launch_frac_add_keys(const MatRef& M, const MatRef& G, int64_t count, int tr
     const long long rows_total = M.rows * count;
     const unsigned blocks = (unsigned)((rows_total + 7) / 8);
     auto* kernel = gscale ? frac_add_keys_rows_kernel<true> : frac_add_keys_rows_kernel<false>;
-    kernel<<<blocks, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride,
-                                                             static_cast<const bf16*>(G.ptr), G.ld, G.stride,
-                                                             (int)M.rows, (int)M.cols, (int)count, keys, nf, gscale);
+    kernel<<<blocks, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride, static_cast<const bf16*>(G.ptr),
+                                          G.ld, G.stride, (int)M.rows, (int)M.cols, (int)count, keys, nf, gscale);
   } else {
     cudaMemsetAsync(keys, 0, sizeof(unsigned long long) * KEY_DIGITS * M.cols * count, S(stream));
     cudaMemsetAsync(nf, 0, sizeof(int) * M.cols * count, S(stream));
@@ -1333,16 +1332,14 @@ int launch_frac_add_keys(const MatRef& M, const MatRef& G, int64_t count, int tr
       const int rpc = (int)std::max(64LL, (M.rows + chunks - 1) / chunks);
       dim3 grid((unsigned)col_blocks, (unsigned)((M.rows + rpc - 1) / rpc), (unsigned)count);
       auto* kernel = gscale ? frac_add_keys_cols8_kernel<true> : frac_add_keys_cols8_kernel<false>;
-      kernel<<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride,
-                                                              static_cast<const bf16*>(G.ptr), G.ld, G.stride,
-                                                              (int)M.rows, (int)M.cols, rpc, keys, nf, gscale);
+      kernel<<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride, static_cast<const bf16*>(G.ptr),
+                                          G.ld, G.stride, (int)M.rows, (int)M.cols, rpc, keys, nf, gscale);
     } else {
       const int rpc = 256;
       dim3 grid((unsigned)((M.cols + 255) / 256), (unsigned)((M.rows + rpc - 1) / rpc), (unsigned)count);
       auto* kernel = gscale ? frac_add_keys_cols_kernel<true> : frac_add_keys_cols_kernel<false>;
-      kernel<<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride,
-                                                             static_cast<const bf16*>(G.ptr), G.ld, G.stride,
-                                                             (int)M.rows, (int)M.cols, rpc, keys, nf, gscale);
+      kernel<<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride, static_cast<const bf16*>(G.ptr),
+                                          G.ld, G.stride, (int)M.rows, (int)M.cols, rpc, keys, nf, gscale);
     }
   }
   return check_launch("frac_add_keys", err);
@@ -1480,18 +1477,20 @@ int launch_rownorm_fused_rows(const MatRef& M, const MatRef& G, const MatRef& W,
                               const float* gscale) {
   dim3 grid((unsigned)M.rows, (unsigned)count);
   const int vpt = (int)((M.cols + 2047) / 2048);
-#define GNS_RN_ARGS                                                                                             \
-  static_cast<bf16*>(M.ptr), M.ld, M.stride, static_cast<const bf16*>(G.ptr), G.ld, G.stride,                 \
-      static_cast<bf16*>(W.ptr), W.ld, W.stride, (int)M.cols, mu, gamma, eps, alpha, beta, gscale
+#define GNS_RN_LAUNCH(VPT)                                                                                     \
+  (gscale ? rownorm_fused_rows_kernel<VPT, true> : rownorm_fused_rows_kernel<VPT, false>)                      \
+      <<<grid, 256, 0, S(stream)>>>(static_cast<bf16*>(M.ptr), M.ld, M.stride, static_cast<const bf16*>(G.ptr), \
+                                    G.ld, G.stride, static_cast<bf16*>(W.ptr), W.ld, W.stride, (int)M.cols, mu, \
+                                    gamma, eps, alpha, beta, gscale)
   if (vpt <= 1)
-    (gscale ? rownorm_fused_rows_kernel<1, true> : rownorm_fused_rows_kernel<1, false>)<<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
+    GNS_RN_LAUNCH(1);
   else if (vpt <= 2)
-    (gscale ? rownorm_fused_rows_kernel<2, true> : rownorm_fused_rows_kernel<2, false>)<<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
+    GNS_RN_LAUNCH(2);
   else if (vpt <= 4)
-    (gscale ? rownorm_fused_rows_kernel<4, true> : rownorm_fused_rows_kernel<4, false>)<<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
+    GNS_RN_LAUNCH(4);
   else
-    (gscale ? rownorm_fused_rows_kernel<8, true> : rownorm_fused_rows_kernel<8, false>)<<<grid, 256, 0, S(stream)>>>(GNS_RN_ARGS);
-#undef GNS_RN_ARGS
+    GNS_RN_LAUNCH(8);
+#undef GNS_RN_LAUNCH
   return check_launch("rownorm_fused_rows", err);
 }
 

@@ -1109,7 +1109,8 @@ int gns_muon_step_scaled(const gns_batch* W, const gns_batch* G, const gns_batch
           return fail(rc, err);
         continue;
       }
-      if ((rc = launch_momentum(mm, gm, s.B, mu, 0, nullptr, stream, &err, nullptr, 0, grad_scale))) return fail(rc, err);
+      if ((rc = launch_momentum(mm, gm, s.B, mu, 0, nullptr, stream, &err, nullptr, 0, grad_scale)))
+        return fail(rc, err);
       if (!s.trans)
         rc = launch_row_sumsq(mm, s.rows, s.cols, s.B, mb.s, stream, &err);
       else
@@ -1211,7 +1212,8 @@ int gns_muon_step_scaled(const gns_batch* W, const gns_batch* G, const gns_batch
     // Dion3 Algorithm 4
     const int64_t k = mb.k;
     // M <- M + G, with the exact l1 keys of the oriented rows
-    if ((rc = launch_frac_add_keys(mm, gm, s.B, s.trans, mb.keys, mb.nf, stream, &err, grad_scale))) return fail(rc, err);
+    if ((rc = launch_frac_add_keys(mm, gm, s.B, s.trans, mb.keys, mb.nf, stream, &err, grad_scale)))
+      return fail(rc, err);
     // selection
     if ((rc = launch_select_topk(mb.keys, mb.nf, s.n, k, s.B, mb.idx, stream, &err))) return fail(rc, err);
     // gather M[S, :] and its Frobenius norm; the error feedback (M[S] <- mu M[S]) rides

@@ -220,8 +220,8 @@ def grad_norm(grads, max_norm: Optional[float] = None, norm_type: float = 2.0, e
     result, ws = _norm_buffers(g, result, workspace, stream)
     cs = _CallStatus(None, g.device, check, stream) if status is None else None
     rc = load().gns_grad_norm(g.address, len(g), code, math.inf if max_norm is None else float(max_norm), float(eps),
-                              result.data_ptr(), ws.data_ptr(), ws.numel(), cs.ptr() if cs else _status_ptr(status, g.index),
-                              _stream(stream, g.index))
+                              result.data_ptr(), ws.data_ptr(), ws.numel(),
+                              cs.ptr() if cs else _status_ptr(status, g.index), _stream(stream, g.index))
     if rc:
         check_rc(rc, "gns_grad_norm")
     if cs:
