@@ -40,7 +40,8 @@
  *   Orientation. A matrix with rows > cols is orthogonalized through its transpose and the
  *     result is mapped back (Dion3 Algorithm 1 assumes n <= m); no transposed copy is made.
  *   Streams. Work is enqueued on `stream` (a cudaStream_t; NULL = legacy default stream)
- *     and returns without synchronising the host. The enqueued work is kernels and memsets
+ *     and returns without synchronising the host. The current device is the one that the
+ *     pointers and the stream belong to. The enqueued work is kernels and memsets
  *     only (a GEMM launch that follows the library's own norm pass may be a programmatic
  *     dependent launch: it starts its setup early and waits on the device for that pass),
  *     so a call may be recorded by stream capture into a CUDA graph and replayed; make

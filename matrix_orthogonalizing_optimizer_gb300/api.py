@@ -4,7 +4,8 @@ stream; every step of the computation runs in the library's CUDA kernels.
 Tensors are CUDA tensors of dtype bfloat16 (hot path), float16 (Dion3 Algorithm 3's
 float16 products) or float32 (validation path), 2-D (one matrix) or 3-D (a batch of
 same-shape matrices, the megabatch of Dion3 sec. 7), with a contiguous last dimension,
-16-byte aligned rows (ld a multiple of 16 bytes) and 16-byte aligned storage.
+16-byte aligned rows (ld a multiple of 16 bytes) and 16-byte aligned storage. Everything that a
+call is given lies on one device, whichever is the current one.
 """
 from __future__ import annotations
 

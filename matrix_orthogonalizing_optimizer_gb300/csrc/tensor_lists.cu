@@ -535,7 +535,9 @@ GNS_DEV uint32_t bits_of(const Vec (&u)[N]) {
 
 // Sum of this thread's squares: up to 64 of a chunk in f32, these sums with the rounding error of
 // each addition kept beside them (Knuth's two-sum), as f32 holds too little for a long list and
-// f64, at 2 operations a clock and SM, took longer than the loads.
+// f64, at 2 operations a clock and SM, took longer than the loads. In units of 2^-24 a chunk's sum is
+// within 33 (two sums of 32, joined), both parts joined 1, a warp's and a block's sums 13, the slots of
+// one launch 3 and 13: 63 of the sum of squares, 32 of the norm, and 2 for the root and its power of two.
 template <bool SCALED, class L>
 GNS_DEV float sum_squares(const L& l, float pre, uint32_t* bits) {
   float s = 0.f, lost = 0.f;
@@ -898,8 +900,9 @@ __global__ void __launch_bounds__(THREADS, L::kRows ? CLIP_ROW_BLOCKS : CLIP_BLO
 
 // A chunk is 4 KB here and every chunk has a warp of its own, which keeps it in registers between
 // its sum and the scaled store: the list is read once. The blocks' shares meet in shared memory.
-// What this saves is a launch on the host: a call takes 8.2 us where the two kernels above take 12
-// (both about 5.3 us on the GPU, at 0.2 MB); the norm alone is one launch anyway.
+// What this saves is a launch on the host: a call takes 6.2 us where the two kernels above take 8.4
+// (4.7 and 4.9 us on the GPU, at 0.2 MB); the norm alone is one launch anyway. The sums are plain
+// f32 ones in another order than norm_kernel's, so the norm's last bit may differ from grad_norm's.
 constexpr int SHORT_THREADS = 512, SHORT_VEC = 8, SHORT_CLUSTER = 8;
 constexpr int SHORT_CHUNKS = SHORT_CLUSTER * SHORT_THREADS / 32;
 
@@ -960,7 +963,7 @@ __global__ void __launch_bounds__(SHORT_THREADS)
 // m <- beta1 m + (1 - beta1) c g;  v <- beta2 v + (1 - beta2) (c g)^2
 // w <- (1 - lr wd) w - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
 //
-// 22 to 28 bytes an element: HBM bounds it (6.5 TB/s read and written on 524 M weights, 96 % of a
+// 22 to 30 bytes an element: HBM bounds it (6.65 TB/s read and written on 524 M weights, 98 % of a
 // copy's rate), with the root and the quotient hidden behind the loads of the other blocks. The
 // moments and masters stay in f32: a 16-bit v loses (1 - beta2) g^2 to rounding. A 16-bit weight is
 // rounded once, from f32. Types are looked at when the loads are out, so one launch takes any mix.
@@ -981,7 +984,9 @@ struct AdamwStep {
   float scale, step_size, rsqrt_bc2;
 };
 
-// The hardware's root and reciprocal, each within 2^-23 of the exact one. The correctly rounded ones
+// The hardware's root and reciprocal, each within 2^-23 of the exact one (an update is then within 13
+// units of 2^-24: half of v's 9, the root 2, its correction and the sum with eps 1 each, the reciprocal
+// 2, the product and the step size 1 each). The correctly rounded ones
 // leave their fast path for zeros and subnormals, and an embedding is full of them: rows that no
 // token has touched have v = 0, and m falls below 2^-126 some 800 steps after the last gradient (66 M
 // embedding weights of which 70 % get no gradient: 304 us with them, 290 with these).

@@ -4,7 +4,8 @@ and the AdamW step of the parameters beside Muon's matrices (embeddings, heads, 
 A list may mix shapes and dtypes (bfloat16, float16, float32). Its tensors are CUDA tensors
 without gaps in memory (contiguous, or a permutation of a contiguous tensor such as a
 transpose), or batches of rows with a pitch: leading dimensions that collapse to one, then
-rows, then a contiguous last dimension. They may start at any element. Every call takes a
+rows, then a contiguous last dimension. They may start at any element. Everything that a call is
+given lies on one device, whichever is the current one. Every call takes a
 plain sequence of tensors or a TensorList, which describes the tensors to the library once; a
 program that keeps its parameters, states and gradients in the same buffers keeps their
 TensorLists too.
