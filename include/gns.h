@@ -114,6 +114,33 @@ typedef struct {
   int32_t reserved;
 } gns_tensor;
 
+/* Microscaled 4-bit floating point: a value is one of +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} (e2m1) times the
+ * scale d of its block, a run of values along a row. */
+typedef enum {
+  GNS_NVFP4 = 0, /* blocks of 16, d = g s: s in e4m3, g one fp32 number of the matrix */
+  GNS_MXFP4 = 1  /* blocks of 32, d a power of two in 8 bits (e8m0) */
+} gns_fp4_format;
+
+/* A batch of matrices held in 4 bits.
+ *   codes         element (b, i, j) is half a byte, the half's place being ptr + (b*stride + i*ld + j) / 2,
+ *                 the low half for even j. ptr 16-byte aligned; ld and stride multiples of 32
+ *                 elements (16 bytes). Codes of columns from cols up to the next multiple of 32 are 0.
+ *   scales        16-byte aligned, per matrix ceil(rows / 128) x ceil(blocks / 4) tiles of 512 bytes
+ *                 (blocks = ceil(cols / 16) or ceil(cols / 32)), tiles of one row of tiles side by
+ *                 side; in its tile, row r's block k has byte (r % 32) * 16 + (r % 128) / 32 * 4 + k % 4.
+ *                 Scales behind the last block are 0 (e8m0: any power of two); those behind the last row
+ *                 are not read.
+ *   scale_stride  bytes between the scales of two matrices, a multiple of 16 (ignored when count == 1)
+ *   tensor_scale  count fp32 numbers g >= 0; NULL for GNS_MXFP4 */
+typedef struct {
+  gns_batch codes;
+  void* scales;
+  int64_t scale_stride;
+  float* tensor_scale;
+  int32_t format;
+  int32_t reserved;
+} gns_fp4;
+
 /* Norm of a list of gradients. */
 typedef enum {
   GNS_NORM_L2 = 0, /* square root of the sum of squares of all elements */
@@ -331,6 +358,47 @@ GNS_API int gns_clip_grads(const gns_tensor* grads, const gns_tensor* outs, int 
 GNS_API int gns_adamw_step(const gns_tensor* W, const gns_tensor* G, const gns_tensor* M, const gns_tensor* V,
                            const gns_tensor* master, int n, const gns_adamw_params* adamw, const float* grad_scale,
                            const int32_t* step_count, int32_t* dev_status, void* stream);
+
+/* ---- matrices in microscaled 4-bit floating point ----
+ *
+ * For weights, activations and gradients around the optimizer step: a step's new weights go into
+ * 4 bits along their rows for the forward product and along their columns for the backward one.
+ * Batches follow the conventions at the top; 4-bit batches are described by gns_fp4. */
+
+/* Bytes of the scales of one rows x cols matrix (0 and the last error on invalid arguments). */
+GNS_API size_t gns_fp4_scale_bytes(int64_t rows, int64_t cols, int format);
+
+/* Brings x (bf16, fp16 or fp32) into 4 bits: into q along its rows (q has x's shape), into qt along
+ * its columns (qt has the shape of the transpose, and holds it), or into both with one reading;
+ * either may be NULL. Both are of one format. With a = max |block|:
+ *   GNS_NVFP4  g = the smallest power of two (at least 2^-126) with max |X| <= 6 * 448 * g, 0 for
+ *              X = 0; s = a / (6 g) rounded to e4m3; codes: x / (g s) rounded to e2m1
+ *   GNS_MXFP4  d = 2^(floor(log2(a)) - 2), the exponent at least -127; codes: x / d rounded to e2m1
+ * Every rounding is to nearest, ties to even, of the exact quotient; magnitudes beyond the largest
+ * value of the type become that value. amax (nullable, device, count floats; GNS_NVFP4 only): max |X| is
+ * read from there, e.g. an earlier step's, and one pass over x is saved; values that exceed it by
+ * much saturate; a number that is not positive and finite there gives g = 1. A block that holds
+ * Inf or NaN gets a NaN scale, which makes the products of its row NaN, and sets GNS_DEVST_NONFINITE;
+ * g is that of the finite values. */
+GNS_API int gns_fp4_quantize(const gns_batch* x, gns_dtype dtype, const gns_fp4* q, const gns_fp4* qt,
+                             const float* amax, int32_t* dev_status, void* stream);
+
+/* The values of q in bf16, fp16 or fp32, each rounded once. */
+GNS_API int gns_fp4_dequantize(const gns_fp4* q, const gns_batch* out, gns_dtype dtype, void* stream);
+
+/* D <- alpha A B^T + beta C, (A B^T)_ij = sum_k A_ik B_jk, for every matrix of the batch: A is m x k,
+ * B n x k, C and D m x n of type `dtype` (bf16, fp16 or fp32). Sums in fp32, one rounding. c may be
+ * NULL when beta == 0; d may be c. A and B are of one format. The gradients of a product y = x w^T
+ * are such products of operands held along their other axis: dx = dy w takes w's qt, dw = dy^T x
+ * the qt of dy and of x. A stored value that is not finite sets GNS_DEVST_NONFINITE. */
+GNS_API int gns_fp4_gemm(const gns_fp4* a, const gns_fp4* b, const gns_batch* c, const gns_batch* d, float alpha,
+                         float beta, gns_dtype dtype, int32_t* dev_status, void* stream);
+
+/* Symmetric rank-K product D <- alpha X X^T + beta C of a batch held in 4 bits (gns_sym_gemm_xxt):
+ * upper tiles are computed and mirrored. C, which must be symmetric, may be NULL when beta == 0;
+ * d may be c. */
+GNS_API int gns_fp4_sym_gemm_xxt(const gns_fp4* x, const gns_batch* c, const gns_batch* d, float alpha, float beta,
+                                 gns_dtype dtype, int32_t* dev_status, void* stream);
 
 /* Self-test of the failure detection every kernel of the library relies on (no GPU fault is
  * involved). Launches one thread that waits, through the same bounded-wait code the GEMM

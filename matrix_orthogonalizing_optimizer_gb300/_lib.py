@@ -27,6 +27,8 @@ GNS_OP_MUON_STEP = 2
 GNS_OP_FRAC_SELECT = 3
 GNS_NORM_L2 = 0
 GNS_NORM_INF = 1
+GNS_NVFP4 = 0
+GNS_MXFP4 = 1
 GNS_MAX_T = 16
 GNS_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -37,6 +39,7 @@ EXPORTS = [
     "gns_sym_poly_update", "gns_muon_step", "gns_frac_row_select", "gns_profile_set", "gns_profile_query", "gns_gram_ns_batched_noalloc",
     "gns_selftest_bounded_wait", "gns_selftest_norm_wait",
     "gns_muon_step_scaled", "gns_list_workspace_size", "gns_grad_norm", "gns_clip_grads", "gns_adamw_step",
+    "gns_fp4_scale_bytes", "gns_fp4_quantize", "gns_fp4_dequantize", "gns_fp4_gemm", "gns_fp4_sym_gemm_xxt",
 ]
 
 
@@ -47,6 +50,11 @@ class GnsBatch(ctypes.Structure):
 
 class GnsTensor(ctypes.Structure):
     _fields_ = [("x", GnsBatch), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class GnsFp4(ctypes.Structure):
+    _fields_ = [("codes", GnsBatch), ("scales", ctypes.c_void_p), ("scale_stride", ctypes.c_int64),
+                ("tensor_scale", ctypes.c_void_p), ("format", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class GnsAdamwParams(ctypes.Structure):
@@ -134,6 +142,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gns_clip_grads.argtypes = [vp, vp, i32, i32, f32, f32, vp, vp, sz, vp, vp]
     lib.gns_adamw_step.restype = i32
     lib.gns_adamw_step.argtypes = [vp, vp, vp, vp, vp, i32, P(GnsAdamwParams), vp, vp, vp, vp]
+    F4 = P(GnsFp4)
+    lib.gns_fp4_scale_bytes.restype = sz
+    lib.gns_fp4_scale_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, i32]
+    lib.gns_fp4_quantize.restype = i32
+    lib.gns_fp4_quantize.argtypes = [B, i32, F4, F4, vp, vp, vp]
+    lib.gns_fp4_dequantize.restype = i32
+    lib.gns_fp4_dequantize.argtypes = [F4, B, i32, vp]
+    lib.gns_fp4_gemm.restype = i32
+    lib.gns_fp4_gemm.argtypes = [F4, F4, B, B, f32, f32, i32, vp, vp]
+    lib.gns_fp4_sym_gemm_xxt.restype = i32
+    lib.gns_fp4_sym_gemm_xxt.argtypes = [F4, B, B, f32, f32, i32, vp, vp]
     lib.gns_selftest_bounded_wait.restype = i32
     lib.gns_selftest_bounded_wait.argtypes = [vp, i32, ctypes.c_uint32, vp, vp, vp]
     lib.gns_selftest_norm_wait.restype = i32

@@ -110,8 +110,9 @@ def batch_of(t: torch.Tensor) -> GnsBatch:
     b = GnsBatch()
     b.ptr = t3.data_ptr()
     b.count, b.rows, b.cols = t3.shape
-    # a single row has no row stride of its own: any ld >= cols that keeps rows aligned
-    b.ld = t3.stride(1) if t3.shape[1] > 1 else ((b.cols + 7) // 8) * 8
+    # a single row has no row stride of its own: the smallest ld >= cols that keeps rows aligned
+    al = 16 // t3.dtype.itemsize
+    b.ld = t3.stride(1) if t3.shape[1] > 1 else (b.cols + al - 1) // al * al
     b.stride = t3.stride(0) if t3.shape[0] > 1 else b.rows * b.ld
     return b
 

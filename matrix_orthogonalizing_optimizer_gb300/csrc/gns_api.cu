@@ -13,6 +13,7 @@
 #include "../../include/gns.h"
 #include "chain_small.h"
 #include "elementwise.h"
+#include "fp4.h"
 #include "gemm.h"
 
 namespace gns {
@@ -181,7 +182,7 @@ static MatRef to_ref(const gns_batch& b) {
 
 static size_t elem_size(gns_dtype dt) { return dt == GNS_F32 ? 4 : 2; }
 
-static int check_batch(const gns_batch* b, gns_dtype dt, const char* name) {
+int check_batch(const gns_batch* b, gns_dtype dt, const char* name) {
   if (!b) return fail(GNS_ERR_INVALID, std::string(name) + ": null batch descriptor");
   const int64_t al = dt == GNS_F32 ? 4 : 8;
   if (!b->ptr) return fail(GNS_ERR_INVALID, std::string(name) + ": null data pointer");
