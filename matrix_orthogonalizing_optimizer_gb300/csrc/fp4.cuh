@@ -78,4 +78,87 @@ GNS_DEV uint32_t fp4_tensor_scale_bits(uint32_t amax_bits) {
 // 1 / g of a power of two 2^-126 <= g <= 2^126.
 GNS_DEV float pow2_inverse(float g) { return __uint_as_float((254u << 23) - __float_as_uint(g)); }
 
+// ---- block-scaled tensor-core products (tcgen05) ----
+
+// Instruction descriptor of kind::mxf4 / mxf4nvf4: both operands e2m1 and K-major, fp32
+// accumulator, M x N x 64. Scales: e4m3 (NVFP4) or e8m0; sf_id: which byte of a scale column's words
+// holds the step's first scale.
+__host__ __device__ constexpr uint32_t fp4_idesc(int fmt, int M, int N, int sf_id) {
+  return (static_cast<uint32_t>(sf_id) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         ((fmt == GNS_NVFP4 ? 0u : 1u) << 23) | (static_cast<uint32_t>(M >> 4) << 24) |
+         (static_cast<uint32_t>(sf_id) << 29);
+}
+
+// Shared-memory descriptor of a 512-byte scale tile for tcgen05.cp: no swizzle, 8 rows of 16 bytes
+// to a core matrix, core matrices 128 bytes apart.
+GNS_DEV uint64_t fp4_scale_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46);
+}
+
+// One scale tile into four tensor-memory columns of all 128 lanes (32 lanes, repeated four times).
+template <int CG>
+GNS_DEV void fp4_copy_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// D[tmem] (+)= (A d_A) (B d_B)^T over 64 values of K.
+template <int FMT, int CG>
+GNS_DEV void fp4_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                     uint32_t accumulate) {
+#define GNS_FP4_MMA(cg, kind, vec)                                                             \
+  asm volatile(                                                                                \
+      "{\n\t.reg .pred p;\n\t"                                                                 \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                              \
+      "tcgen05.mma.cta_group::" cg ".kind::" kind ".block_scale.scale_vec::" vec               \
+      " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                       \
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                          \
+      : "memory")
+  if constexpr (FMT == GNS_NVFP4 && CG == 2)
+    GNS_FP4_MMA("2", "mxf4nvf4", "4X");
+  else if constexpr (FMT == GNS_NVFP4)
+    GNS_FP4_MMA("1", "mxf4nvf4", "4X");
+  else if constexpr (CG == 2)
+    GNS_FP4_MMA("2", "mxf4", "2X");
+  else
+    GNS_FP4_MMA("1", "mxf4", "2X");
+#undef GNS_FP4_MMA
+}
+
+// 4-D TMA load; completion on the mbarrier at shared::cluster address `bar` (the leader's for a
+// CTA pair).
+template <int CG>
+GNS_DEV void fp4_tma_load_4d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2, int c3) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+template <int CG>
+GNS_DEV void fp4_tma_load_3d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1, int c2) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
 }  // namespace gns
