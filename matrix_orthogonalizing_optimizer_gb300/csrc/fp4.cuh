@@ -80,6 +80,26 @@ GNS_DEV float pow2_inverse(float g) { return __uint_as_float((254u << 23) - __fl
 
 // ---- block-scaled tensor-core products (tcgen05) ----
 
+// mbar_wait without its clock read on the way: the timer is first read after 64 tries. A slice of 4-bit
+// operands is a few hundred cycles of tensor-core work, and a read of the global timer costs about as much.
+GNS_DEV bool fp4_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  const uint32_t a = smem_u32(bar);
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(a, parity)) return true;
+  return mbar_wait(bar, parity, abort_flag, status);
+}
+
+// One lane of a converged warp, the same one each time.
+GNS_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Instruction descriptor of kind::mxf4 / mxf4nvf4: both operands e2m1 and K-major, fp32
 // accumulator, M x N x 64. Scales: e4m3 (NVFP4) or e8m0; sf_id: which byte of a scale column's words
 // holds the step's first scale.

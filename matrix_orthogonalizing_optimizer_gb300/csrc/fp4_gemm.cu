@@ -14,6 +14,7 @@
 // alpha, addend, rounding, a staging buffer in shared memory, TMA stores.
 #include <cudaTypedefs.h>
 
+#include <cstdlib>
 #include <mutex>
 
 #include "fp4.cuh"
@@ -114,23 +115,75 @@ GNS_DEV uint32_t pack2(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Whether one of two stored 16-bit values (a word) is Inf or NaN.
+// x 0 + sum, on two 16-bit values: NaN from the first Inf or NaN on.
 template <int DT>
-GNS_DEV bool nonfinite2(uint32_t w) {
-  constexpr uint32_t E = DT == GNS_F16 ? 0x7C00u : 0x7F80u;
-  return (w & E) == E || ((w >> 16) & E) == E;
+GNS_DEV uint32_t probe2(uint32_t x, uint32_t sum) {
+  if (DT == GNS_F16) {
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(0.f), *reinterpret_cast<const __half2*>(&sum));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const __nv_bfloat162 r =
+      __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), __float2bfloat162_rn(0.f), *reinterpret_cast<const __nv_bfloat162*>(&sum));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Whether one of the first `valid` of a row's stored values (128 bytes in w) is Inf or NaN.
+template <int DT>
+GNS_DEV bool any_nonfinite(const uint32_t (&w)[32], int valid) {
+  constexpr int CW = DT == GNS_F32 ? 32 : 64;
+  if (valid >= CW) {
+    if (DT == GNS_F32) {
+      float2 z = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        z = __ffma2_rn(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), make_float2(0.f, 0.f), z);
+      return !(z.x == 0.f && z.y == 0.f);
+    }
+    uint32_t z = 0u;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) z = probe2<DT>(w[i], z);
+    return (z & 0x7FFF7FFFu) != 0u;
+  }
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (DT == GNS_F32) {
+      bad |= i < valid && (w[i] & 0x7F800000u) == 0x7F800000u;
+    } else {
+      constexpr uint32_t E = DT == GNS_F16 ? 0x7C00u : 0x7F80u;
+      bad |= 2 * i < valid && (w[i] & E) == E;
+      bad |= 2 * i + 1 < valid && ((w[i] >> 16) & E) == E;
+    }
+  }
+  return bad;
+}
+
+// alpha and the matrices' scales as one factor, or as two where their product leaves fp32's normal range.
+struct Factor {
+  float one, two;
+  bool split;
+};
+GNS_DEV Factor factor_of(const GemmParams& P, int b) {
+  const float sa = P.ga ? P.alpha * P.ga[b] : P.alpha, sb = P.gb ? P.gb[b] : 1.f;
+  const float f = sa * sb;
+  Factor o;
+  o.split = !(fabsf(f) >= 1.17549435e-38f && fabsf(f) <= 3.4e38f);
+  o.one = o.split ? sa : f;
+  o.two = sb;
+  return o;
 }
 
 // A warp's 32 rows of the tile, chunk by chunk (DT: the type of C and D).
 template <int DT, int BN>
 GNS_DEV bool epilogue_tile(const GemmParams& P, const Tile& t, uint32_t acc, int row0, int n0, uint8_t* out, uint64_t* cbar,
-                           uint32_t& chunk, float sa, float sb, bool mirror, int lane, volatile int* abort_flag) {
+                           uint32_t& chunk, const Factor& f, bool mirror, int lane, volatile int* abort_flag) {
   constexpr int CW = DT == GNS_F32 ? 32 : 64;  // columns of a chunk
   bool bad = false;
   const bool rows_in = row0 < P.M;
   const int ncols = min(BN, P.N - n0);
   const int nch = rows_in ? (ncols + CW - 1) / CW : 0;
-  if (P.has_c && nch > 0) {
+  if (nch == 0) return false;
+  if (P.has_c) {
     if (lane == 0) {
       bulk_wait_read<1>();
       mbar_arrive_expect_tx(&cbar[chunk & 1], OUT_BYTES);
@@ -138,50 +191,54 @@ GNS_DEV bool epilogue_tile(const GemmParams& P, const Tile& t, uint32_t acc, int
     }
     __syncwarp();
   }
+  uint32_t r[CW / 32][32];
+#pragma unroll
+  for (int h = 0; h < CW / 32; ++h) tmem_ld_32x32b_x32(acc + 32 * h, r[h]);
   for (int ch = 0; ch < nch; ++ch, ++chunk) {
     uint8_t* const buf = out + (chunk & 1) * OUT_BYTES;
-    uint32_t r[CW / 32][32];
-#pragma unroll
-    for (int h = 0; h < CW / 32; ++h) tmem_ld_32x32b_x32(acc + ch * CW + 32 * h, r[h]);
     tmem_ld_wait();
-    float v[CW];
+    float2 v[CW / 2];
+    const float2 f1 = make_float2(f.one, f.one);
 #pragma unroll
-    for (int i = 0; i < CW; ++i) v[i] = __uint_as_float(r[i / 32][i % 32]) * sa * sb;
+    for (int i = 0; i < CW / 2; ++i)
+      v[i] = __fmul2_rn(make_float2(__uint_as_float(r[i / 16][2 * i % 32]), __uint_as_float(r[i / 16][2 * i % 32 + 1])), f1);
+    if (ch + 1 < nch) {  // the next chunk's values are on their way while this one is rounded and stored
+#pragma unroll
+      for (int h = 0; h < CW / 32; ++h) tmem_ld_32x32b_x32(acc + (ch + 1) * CW + 32 * h, r[h]);
+    }
+    if (f.split) {
+#pragma unroll
+      for (int i = 0; i < CW / 2; ++i) v[i] = __fmul2_rn(v[i], make_float2(f.two, f.two));
+    }
     if (!P.has_c) {
       if (lane == 0) bulk_wait_read<1>();
       __syncwarp();
     } else {
-      if (!mbar_wait(&cbar[chunk & 1], (chunk >> 1) & 1u, abort_flag, P.status)) return bad;
+      if (!fp4_wait(&cbar[chunk & 1], (chunk >> 1) & 1u, abort_flag, P.status)) return bad;
+      const float2 b2 = make_float2(P.beta, P.beta);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const uint4 w = *reinterpret_cast<const uint4*>(buf + out_at(lane, u));
-        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+        if (DT == GNS_F32) {
+          v[2 * u] = __ffma2_rn(b2, make_float2(__uint_as_float(w.x), __uint_as_float(w.y)), v[2 * u]);
+          v[2 * u + 1] = __ffma2_rn(b2, make_float2(__uint_as_float(w.z), __uint_as_float(w.w)), v[2 * u + 1]);
+        } else {
+          const uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (DT == GNS_F32) {
-            v[4 * u + i] += P.beta * __uint_as_float(e[i]);
-          } else {
-            const float2 c = unpack2<DT>(e[i]);
-            v[(8 * u + 2 * i) % CW] += P.beta * c.x;
-            v[(8 * u + 2 * i + 1) % CW] += P.beta * c.y;
-          }
+          for (int i = 0; i < 4; ++i) v[(4 * u + i) % (CW / 2)] = __ffma2_rn(b2, unpack2<DT>(e[i]), v[(4 * u + i) % (CW / 2)]);
         }
       }
     }
     uint32_t w[32];  // the row's 128 bytes
 #pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = DT == GNS_F32 ? __float_as_uint(v[i]) : pack2<DT>(v[(2 * i) % CW], v[(2 * i + 1) % CW]);
-    // rows and columns outside the matrix hold nothing of it
-    if (row0 + lane < P.M) {
-      const int valid = ncols - ch * CW;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if (DT == GNS_F32)
-          bad |= i < valid && (w[i] & 0x7F800000u) == 0x7F800000u;
-        else
-          bad |= 2 * i < valid && nonfinite2<DT>(2 * i + 1 < valid ? w[i] : w[i] & 0xFFFFu);
-      }
+    for (int i = 0; i < 32; ++i) {
+      if (DT == GNS_F32)
+        w[i] = __float_as_uint(i & 1 ? v[i / 2].y : v[i / 2].x);
+      else
+        w[i] = pack2<DT>(v[i % (CW / 2)].x, v[i % (CW / 2)].y);
     }
+    // rows and columns outside the matrix hold nothing of it
+    if (row0 + lane < P.M) bad |= any_nonfinite<DT>(w, ncols - ch * CW);
 #pragma unroll
     for (int u = 0; u < 8; ++u)
       *reinterpret_cast<uint4*>(buf + out_at(lane, u)) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
@@ -286,7 +343,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
         const int m0 = t.I * TM * CG + (int)rank * TM;
         const int n0 = t.J * BN;
         for (int kb = 0; kb < P.kblocks; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag, P.status)) {
+          if (!fp4_wait(&empty[s], ph ^ 1u, abort_flag, P.status)) {
             ok = false;
             break;
           }
@@ -306,10 +363,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      const uint32_t base = smem_u32(smem);
-      const uint32_t sfa_t = tmem + L::NACC * BN;
+    if (rank == 0) {
+      // The whole warp walks the slices, and one elected lane issues: the operands of copies and MMAs
+      // then are in uniform registers. From a lane of its own, in divergent code, each of the 12 to 16
+      // instructions of a slice took 55 to 75 cycles to issue, more than the tensor cores need.
+      const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_u32(smem), 0);
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const uint32_t sfa_t = tm + L::NACC * BN;
       const uint32_t sfb_t = sfa_t + 4 * L::KT;
+      const bool leader = elect_one();
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -317,48 +379,55 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
       for (long long tile = group; ok && tile < P.total; tile += ngroups, ++local) {
         const int acc = local % L::NACC;
         const uint32_t aph = (local / L::NACC) & 1;
-        if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, P.status)) break;
+        if (!fp4_wait(&tempty[acc], aph ^ 1u, abort_flag, P.status)) break;
         tc_fence_after();
-        const uint32_t d = tmem + acc * BN;
+        const uint32_t d = tm + acc * BN;
+        // B's first row in its first scale tile: 32 rows to a column
+        const uint32_t sfb_0 = sfb_t + (BN % 128 ? (tile_of(P, tile).J * BN % 128) / 32 : 0);
         for (int kb = 0; kb < P.kblocks; ++kb) {
-          if (!mbar_wait(&full[s], ph, abort_flag, P.status)) {
+          if (!fp4_wait(&full[s], ph, abort_flag, P.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sa = base + s * (L::A_BYTES + L::B_BYTES);
           const uint32_t sf = base + L::OFF_SF + s * (L::SFA_BYTES + L::SFB_BYTES);
-#pragma unroll
-          for (int k = 0; k < L::KT; ++k) {
-            fp4_copy_scales<CG>(sfa_t + 4 * k, fp4_scale_desc(sf + 512 * k));
-#pragma unroll
-            for (int n = 0; n < L::BT; ++n)
-              fp4_copy_scales<CG>(sfb_t + 4 * (k * L::BT + n), fp4_scale_desc(sf + L::SFA_BYTES + 512 * (n * L::KT + k)));
-          }
+          const uint64_t sfd = fp4_scale_desc(sf);
           const uint64_t ad = sdesc_sw128(sa, 16, 1024), bd = sdesc_sw128(sa + L::A_BYTES, 16, 1024);
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < TK / 64; ++kk) {
-            // a scale column's word has the scales of 64 values (NVFP4) or 128 (MXFP4)
-            constexpr int PER = fp4_block(FMT) / 16;
-            const int k = kk / PER, id = (kk % PER) * 2;
-            fp4_mma<FMT, CG>(d, ad + 2 * kk, bd + 2 * kk, fp4_idesc(FMT, TM * CG, BN, id), sfa_t + 4 * k,
-                             sfb_t + 4 * k * L::BT, (kb | kk) != 0 ? 1u : 0u);
+            for (int k = 0; k < L::KT; ++k) {
+              fp4_copy_scales<CG>(sfa_t + 4 * k, sfd + 32 * k);
+#pragma unroll
+              for (int n = 0; n < L::BT; ++n)
+                fp4_copy_scales<CG>(sfb_t + 4 * (k * L::BT + n), sfd + L::SFA_BYTES / 16 + 32 * (n * L::KT + k));
+            }
+#pragma unroll
+            for (int kk = 0; kk < TK / 64; ++kk) {
+              // a scale column's word has the scales of 64 values (NVFP4) or 128 (MXFP4)
+              constexpr int PER = fp4_block(FMT) / 16;
+              const int k = kk / PER, id = (kk % PER) * 2;
+              fp4_mma<FMT, CG>(d, ad + 2 * kk, bd + 2 * kk, fp4_idesc(FMT, TM * CG, BN, id), sfa_t + 4 * k,
+                               sfb_0 + 4 * k * L::BT, (kb | kk) != 0 ? 1u : 0u);
+            }
+            if constexpr (CG == 2)
+              umma2_commit_multicast(&empty[s], 0x3);
+            else
+              umma_commit(&empty[s]);
           }
-          if constexpr (CG == 2)
-            umma2_commit_multicast(&empty[s], 0x3);
-          else
-            umma_commit(&empty[s]);
+          __syncwarp();
           if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
-        if (ok) {
+        if (ok && leader) {
           if constexpr (CG == 2)
             umma2_commit_multicast(&tfull[acc], 0x3);
           else
             umma_commit(&tfull[acc]);
         }
+        __syncwarp();
       }
     }
   } else if (warp >= EPI_WARP) {
@@ -372,9 +441,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
       const Tile t = tile_of(P, tile);
       const int acc = local % L::NACC;
       const uint32_t aph = (local / L::NACC) & 1;
-      const float sa = P.ga ? P.alpha * P.ga[t.b] : P.alpha;
-      const float sb = P.gb ? P.gb[t.b] : 1.f;
-      if (!mbar_wait(&tfull[acc], aph, abort_flag, P.status)) break;
+      const Factor f = factor_of(P, t.b);
+      if (!fp4_wait(&tfull[acc], aph, abort_flag, P.status)) break;
       tc_fence_after();
       __syncwarp();
       const int row0 = t.I * TM * CG + (int)rank * TM + 32 * q;
@@ -382,11 +450,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
       const bool mirror = P.sym && t.I != t.J;
       uint64_t* const cb = cbar + 2 * q;
       if (P.dtype == GNS_BF16)
-        bad |= epilogue_tile<GNS_BF16, BN>(P, t, at, row0, t.J * BN, out, cb, chunk, sa, sb, mirror, lane, abort_flag);
+        bad |= epilogue_tile<GNS_BF16, BN>(P, t, at, row0, t.J * BN, out, cb, chunk, f, mirror, lane, abort_flag);
       else if (P.dtype == GNS_F16)
-        bad |= epilogue_tile<GNS_F16, BN>(P, t, at, row0, t.J * BN, out, cb, chunk, sa, sb, mirror, lane, abort_flag);
+        bad |= epilogue_tile<GNS_F16, BN>(P, t, at, row0, t.J * BN, out, cb, chunk, f, mirror, lane, abort_flag);
       else
-        bad |= epilogue_tile<GNS_F32, BN>(P, t, at, row0, t.J * BN, out, cb, chunk, sa, sb, mirror, lane, abort_flag);
+        bad |= epilogue_tile<GNS_F32, BN>(P, t, at, row0, t.J * BN, out, cb, chunk, f, mirror, lane, abort_flag);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -540,6 +608,13 @@ int launch(const Fp4Product& p, int32_t* status, cudaStream_t stream, std::strin
 
 template <int FMT>
 int launch_format(const Fp4Product& p, int32_t* status, cudaStream_t stream, std::string* err) {
+  const char* e = getenv("GNS_FP4_TILE");
+  const int v = e ? atoi(e) : 0;
+  if (v == 1) return launch<FMT, 2, 256>(p, status, stream, err);
+  if (v == 2 && !p.sym) return launch<FMT, 2, 128>(p, status, stream, err);
+  if (v == 3 && !p.sym) return launch<FMT, 1, 256>(p, status, stream, err);
+  if (v == 5 && !p.sym) return launch<FMT, 2, 192>(p, status, stream, err);
+  if (v == 4 && !p.sym) return launch<FMT, 1, 64>(p, status, stream, err);
   return launch<FMT, 1, 128>(p, status, stream, err);
 }
 
