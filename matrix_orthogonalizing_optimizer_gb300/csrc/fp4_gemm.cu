@@ -14,7 +14,6 @@
 // alpha, addend, rounding, a staging buffer in shared memory, TMA stores.
 #include <cudaTypedefs.h>
 
-#include <cstdlib>
 #include <mutex>
 
 #include "fp4.cuh"
@@ -606,15 +605,27 @@ int launch(const Fp4Product& p, int32_t* status, cudaStream_t stream, std::strin
   return GNS_OK;
 }
 
+// 128 x 128 tiles of single CTAs, or tiles of CTA pairs: 256 x 192 (two accumulators in tensor memory) for
+// A B^T, 256 x 256 (one accumulator; a symmetric product's tiles are square) for X X^T. A pair tile
+// reads less per product from L2, which bounds the small one, and fills the SMs less evenly. What counts is
+// the number of waves over the SMs, weighted by what one costs (measured, K from 4096 to 8192: a wave of
+// 256 x 192 tiles takes about 1.1, of 256 x 256 tiles 1.6 to 1.9 times one of 128 x 128). bf16 results,
+// 128 x 128 against the pair's, us: 16384 x 11008 x 4096 378 / 273, 4096 x 11008 x 4096 103 / 76, 512 x 4096 x
+// 4096 9.4 / 11.0, 16 of 1024 x 1024 x 2048 25.5 / 28.8; X X^T of 16 of 2048 x 8192 151 / 127, of 24 of
+// 1024 x 4096 37.7 / 47.
 template <int FMT>
 int launch_format(const Fp4Product& p, int32_t* status, cudaStream_t stream, std::string* err) {
-  const char* e = getenv("GNS_FP4_TILE");
-  const int v = e ? atoi(e) : 0;
-  if (v == 1) return launch<FMT, 2, 256>(p, status, stream, err);
-  if (v == 2 && !p.sym) return launch<FMT, 2, 128>(p, status, stream, err);
-  if (v == 3 && !p.sym) return launch<FMT, 1, 256>(p, status, stream, err);
-  if (v == 5 && !p.sym) return launch<FMT, 2, 192>(p, status, stream, err);
-  if (v == 4 && !p.sym) return launch<FMT, 1, 64>(p, status, stream, err);
+  const long long sms = device_sm_count(), M = p.a.rows, N = p.b.rows;
+  auto up = [](long long n, long long d) { return (n + d - 1) / d; };
+  auto tri = [](long long t) { return t * (t + 1) / 2; };
+  const long long m1 = up(M, 128), m2 = up(M, 256);
+  const long long single = up(p.count * (p.sym ? tri(m1) : m1 * up(N, 128)), sms);
+  const long long pairs = up(p.count * (p.sym ? tri(m2) : m2 * up(N, 192)), sms / 2);
+  if (p.sym) {
+    if (1.75 * (double)pairs < (double)single) return launch<FMT, 2, 256>(p, status, stream, err);
+  } else if (1.2 * (double)pairs < (double)single) {
+    return launch<FMT, 2, 192>(p, status, stream, err);
+  }
   return launch<FMT, 1, 128>(p, status, stream, err);
 }
 

@@ -195,7 +195,7 @@ def check_product(got, a, b, dtype, alpha=1.0, beta=0.0, c=None):
 
 
 PRODUCTS = [(1, 1, 1, 1), (1, 1, 64, 64), (1, 3, 5, 17), (2, 1, 300, 1000), (1, 16, 129, 256), (1, 33, 70, 4100), (3, 129, 127, 65),
-            (1, 128, 128, 512), (2, 257, 130, 300), (1, 300, 520, 1025), (1, 515, 700, 96), (1, 64, 1000, 2048), (1, 1025, 1, 40)]
+            (1, 128, 128, 512), (2, 257, 130, 300), (1, 300, 520, 1025), (1, 515, 700, 96), (1, 64, 1000, 2048), (1, 1025, 1, 40), (1, 300, 11000, 300), (2, 2050, 2100, 130)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -221,7 +221,7 @@ def test_gemm(shape, dtype, fmt):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 5, 100), (1, 128, 512), (3, 130, 300), (2, 333, 2001), (1, 600, 257)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 5, 100), (1, 128, 512), (3, 130, 300), (2, 333, 2001), (1, 600, 257), (1, 5000, 300)], ids=str)
 def test_gram(shape, dtype, fmt):
     x, vx = random_held(21, shape, fmt)
     d = gns.fp4_sym_gemm_xxt(x, alpha=1 / 64, dtype=DTYPES[dtype])
