@@ -387,7 +387,8 @@ GNS_API int gns_fp4_quantize(const gns_batch* x, gns_dtype dtype, const gns_fp4*
 GNS_API int gns_fp4_dequantize(const gns_fp4* q, const gns_batch* out, gns_dtype dtype, void* stream);
 
 /* D <- alpha A B^T + beta C, (A B^T)_ij = sum_k A_ik B_jk, for every matrix of the batch: A is m x k,
- * B n x k, C and D m x n of type `dtype` (bf16, fp16 or fp32). Sums in fp32, one rounding. c may be
+ * B n x k, C and D m x n of type `dtype` (bf16, fp16 or fp32). Sums in fp32 (the tensor cores cut where
+ * others round: sums of one sign come out low by 2e-6 at k = 11008), one rounding. c may be
  * NULL when beta == 0; d may be c. A and B are of one format. The gradients of a product y = x w^T
  * are such products of operands held along their other axis: dx = dy w takes w's qt, dw = dy^T x
  * the qt of dy and of x. A stored value that is not finite sets GNS_DEVST_NONFINITE. */
