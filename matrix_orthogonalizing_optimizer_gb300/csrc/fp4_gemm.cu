@@ -157,18 +157,24 @@ GNS_DEV bool any_nonfinite(const uint32_t (&w)[32], int valid) {
   return bad;
 }
 
-// alpha and the matrices' scales as one factor, or as two where their product leaves fp32's normal range.
+// The sum's factor alpha g_A g_B: formed in 64 bits, which hold every product of three fp32 numbers, and rounded
+// once. Where it leaves fp32's normal range the sum is multiplied by two numbers, the second a power of two that brings
+// the first back into it: as |sum| >= 2^-20 (NVFP4's smallest product) or 0, and < 2^64, neither step leaves the range
+// unless the result does. (MXFP4 has no g; its alpha leaves the normal range as a subnormal only.)
 struct Factor {
   float one, two;
   bool split;
 };
 GNS_DEV Factor factor_of(const GemmParams& P, int b) {
-  const float sa = P.ga ? P.alpha * P.ga[b] : P.alpha, sb = P.gb ? P.gb[b] : 1.f;
-  const float f = sa * sb;
+  constexpr double BIG = 0x1p100, MOST = 3.4028234663852886e38;
+  const double f = (double)P.alpha * (P.ga ? (double)P.ga[b] : 1.0) * (P.gb ? (double)P.gb[b] : 1.0);
+  const double size = fabs(f);
   Factor o;
-  o.split = !(fabsf(f) >= 1.17549435e-38f && fabsf(f) <= 3.4e38f);
-  o.one = o.split ? sa : f;
-  o.two = sb;
+  o.split = !(size >= 0x1p-126 && size <= MOST);
+  o.two = size < 1.0 ? (float)(1.0 / BIG) : (float)BIG;
+  // (beyond 2^228 every sum but 0 gives Inf, and 0 stays 0)
+  const double h = o.split ? f * (size < 1.0 ? BIG : 1.0 / BIG) : f;
+  o.one = (float)(fabs(h) > MOST ? copysign(MOST, h) : h);
   return o;
 }
 
