@@ -131,7 +131,8 @@ typedef enum {
  *                 Scales behind the last block are 0 (e8m0: any power of two); those behind the last row
  *                 are not read.
  *   scale_stride  bytes between the scales of two matrices, a multiple of 16 (ignored when count == 1)
- *   tensor_scale  count fp32 numbers g >= 0; NULL for GNS_MXFP4 */
+ *   tensor_scale  count finite fp32 numbers g >= 0 (gns_fp4_quantize gives powers of two; data from elsewhere may
+ *                 have any other); NULL for GNS_MXFP4 */
 typedef struct {
   gns_batch codes;
   void* scales;

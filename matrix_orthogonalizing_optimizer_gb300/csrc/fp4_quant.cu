@@ -424,7 +424,66 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const __grid_constant
   if (bad) set_status(P.status, GNS_DEVST_NONFINITE);
 }
 
+// v g cut to fp32, its last bit set where something was cut off (round to odd): rounded to a 16-bit type, that is v g
+// rounded once. The rest is formed rounded up, so that it is never lost to underflow.
+GNS_DEV float times_odd(float v, float g) {
+  const float a = fabsf(v), h = fabsf(g), p = __fmul_rz(a, h);
+  const uint32_t odd = __fmaf_ru(a, h, -p) > 0.f ? 1u : 0u;
+  return copysignf(__uint_as_float(__float_as_uint(p) | odd), v) * copysignf(1.f, g);
+}
+
+// The values of a block (those `left` of them that exist). EXACT: g s is exact.
+template <class T, int FMT, bool EXACT>
+GNS_DEV void put_values(const uint32_t (&codes)[FMT == GNS_NVFP4 ? 2 : 4], float s, float g, T* o, int left) {
+  constexpr int N = FMT == GNS_NVFP4 ? 16 : 32;
+  const float d = EXACT ? g * s : s;
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i) {
+    float2 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = __fmul2_rn(e2m1x2_to_f2(codes[i] >> (8 * j)), make_float2(d, d));
+      if constexpr (!EXACT)
+        v[j] = sizeof(T) == 4 ? make_float2(v[j].x * g, v[j].y * g) : make_float2(times_odd(v[j].x, g), times_odd(v[j].y, g));
+    }
+    uint32_t w[8];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(j & 1 ? v[j / 2].y : v[j / 2].x);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (std::is_same<T, __half>::value) {
+          const __half2 h = __float22half2_rn(v[j]);
+          w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __nv_bfloat162 h = __float22bfloat162_rn(v[j]);
+          w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+    }
+    if (left >= 8 * i + 8) {
+      *reinterpret_cast<uint4*>(o + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (sizeof(T) == 4) *(reinterpret_cast<uint4*>(o + 8 * i) + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (8 * i + j < left) {
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<uint32_t*>(o + 8 * i + j) = w[j];
+          else
+            *reinterpret_cast<uint16_t*>(o + 8 * i + j) = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+        }
+    }
+  }
+}
+
 // A thread takes blocks of a row: 8 or 16 bytes of codes and a scale into 16 or 32 values.
+//
+// A code times s has at most 6 bits. With g a power of two (what quantisation gives), or none, g s and the values are exact
+// in fp32 and the conversion to T rounds once. Another g, or one near fp32's ends, is multiplied last: rounded to
+// nearest for fp32, to odd ahead of the rounding to 16 bits. The block's loads come before the question which g it
+// is, so that they do not wait for g.
 template <class T, int FMT>
 __global__ void __launch_bounds__(THREADS) dequantize_kernel(Fp4Ref q, T* out, long long ld, long long stride, int blocks,
                                                              long long total) {
@@ -434,9 +493,7 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(Fp4Ref q, T* out, l
   for (long long id = (long long)blockIdx.x * THREADS + threadIdx.x; id < total; id += (long long)gridDim.x * THREADS) {
     const int row = total < (1ll << 31) ? (int)((uint32_t)id / (uint32_t)blocks) : (int)(id / blocks);
     const int k = (int)(id - (long long)row * blocks);
-    // (g s is exact: g is a power of two, at least 2^-126, and s has 4 bits above 2^-9)
-    const float d = g * fp4_scale_to_f<FMT>(q.scales[b * q.scale_stride + ((long long)(row >> 7) * q.block_tiles + (k >> 2)) * 512 +
-                                                    fp4_scale_at(row, k)]);
+    const uint8_t byte = q.scales[b * q.scale_stride + ((long long)(row >> 7) * q.block_tiles + (k >> 2)) * 512 + fp4_scale_at(row, k)];
     const uint8_t* c = q.codes + b * q.stride + row * q.ld + k * (N / 2);
     uint32_t codes[N / 8];
     if (N == 16) {
@@ -452,41 +509,13 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(Fp4Ref q, T* out, l
     }
     T* o = out + b * stride + row * ld + k * N;
     const int left = q.cols - k * N;
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-      float2 v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(e2m1x2_to_f2(codes[i] >> (8 * j)), make_float2(d, d));
-      uint32_t w[8];
-      if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(j & 1 ? v[j / 2].y : v[j / 2].x);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (std::is_same<T, __half>::value) {
-            const __half2 h = __float22half2_rn(v[j]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&h);
-          } else {
-            const __nv_bfloat162 h = __float22bfloat162_rn(v[j]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-        }
-      }
-      if (left >= 8 * i + 8) {
-        *reinterpret_cast<uint4*>(o + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (sizeof(T) == 4) *(reinterpret_cast<uint4*>(o + 8 * i) + 1) = make_uint4(w[4], w[5], w[6], w[7]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (8 * i + j < left) {
-            if constexpr (sizeof(T) == 4)
-              *reinterpret_cast<uint32_t*>(o + 8 * i + j) = w[j];
-            else
-              *reinterpret_cast<uint16_t*>(o + 8 * i + j) = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
-          }
-      }
-    }
+    const float s = fp4_scale_to_f<FMT>(byte);
+    // g 0, or a power of two from 2^-126 to 2^118: g s is 0, or at least 2^-135 and below 2^127
+    const uint32_t gb = __float_as_uint(g);
+    if (FMT == GNS_MXFP4 || gb == 0u || ((gb & 0x7FFFFFu) == 0u && gb >= 1u << 23 && gb <= (127u + 118u) << 23))
+      put_values<T, FMT, true>(codes, s, g, o, left);
+    else if constexpr (FMT == GNS_NVFP4)
+      put_values<T, FMT, false>(codes, s, g, o, left);
   }
 }
 
