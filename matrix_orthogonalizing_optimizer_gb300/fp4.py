@@ -34,13 +34,19 @@ def _tiles(rows: int, cols: int, fmt: str):
 
 
 class Fp4Matrix:
-    """A matrix (or a batch of them) in 4-bit floating point, as include/gns.h lays it out (gns_fp4).
+    """A matrix (or a batch of them) in 4-bit floating point, as include/gns.h lays it out (gns_fp4). It keeps its
+    tensors alive, and describes the memory that they have when it is made: its attributes cannot be assigned,
+    and a tensor that got new memory needs a new Fp4Matrix.
 
     codes: uint8, (rows, bytes) or (count, rows, bytes), two codes a byte (the first in the low
         half), at least ceil(cols / 32) * 16 bytes a row; rows on 16-byte boundaries.
     scales: uint8, (row tiles, block tiles, 512) or (count, ...), without gaps inside a matrix.
-    tensor_scale: float32, one for each matrix ("nvfp4"), or None ("mxfp4").
+    tensor_scale: float32, one for each matrix ("nvfp4"; a power of two from quantize_fp4, else any finite number that is
+        not negative), or None ("mxfp4").
     cols: values in a row."""
+
+    # addresses and sizes are noted once: the kernels would go on reading the memory of a tensor that was put elsewhere
+    _FIXED = frozenset(("codes", "scales", "tensor_scale", "fmt", "shape", "device", "index", "_struct", "_ref"))
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, tensor_scale: Optional[torch.Tensor], cols: int,
                  fmt: str = "nvfp4"):
@@ -68,11 +74,8 @@ class Fp4Matrix:
                 raise ValueError(f"tensor_scale must be a contiguous float32 tensor of {count} entries")
         elif tensor_scale is not None:
             raise ValueError("mxfp4 has no tensor_scale")
-        self.device = codes.device
-        _one_device(codes.get_device(), scales=scales, tensor_scale=tensor_scale)
-        self.codes, self.scales, self.tensor_scale, self.fmt = codes, scales, tensor_scale, fmt
-        self.shape = torch.Size((*lead, rows, cols))
-        self.index = codes.get_device()
+        index = codes.get_device()
+        _one_device(index, scales=scales, tensor_scale=tensor_scale)
         q = GnsFp4()
         b = q.codes
         b.ptr, b.count, b.rows, b.cols = codes.data_ptr(), count, rows, cols
@@ -82,8 +85,18 @@ class Fp4Matrix:
         q.scale_stride = scales.stride(0) if lead else scales.numel()
         q.tensor_scale = tensor_scale.data_ptr() if tensor_scale is not None else None
         q.format = code
-        self._struct = q
-        self._ref = ctypes.byref(q)
+        self.__dict__.update(codes=codes, scales=scales, tensor_scale=tensor_scale, fmt=fmt, device=codes.device, index=index,
+                             shape=torch.Size((*lead, rows, cols)), _struct=q, _ref=ctypes.byref(q))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED:
+            raise AttributeError(f"{name} of an Fp4Matrix cannot be assigned: make a new one")
+        super().__setattr__(name, value)
+
+    def __delattr__(self, name):
+        if name in self._FIXED:
+            raise AttributeError(f"{name} of an Fp4Matrix cannot be deleted")
+        super().__delattr__(name)
 
     def __repr__(self):
         return f"Fp4Matrix(shape={tuple(self.shape)}, fmt={self.fmt!r}, device='{self.device}')"
