@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "fp4.h"
+#include "fp4_ring.h"
 
 namespace gns {
 
@@ -87,6 +88,37 @@ GNS_DEV bool fp4_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, 
   for (int i = 0; i < 64; ++i)
     if (mbar_try_wait(a, parity)) return true;
   return mbar_wait(bar, parity, abort_flag, status);
+}
+
+// The same for a whole converged warp, which goes on or gives up as one: what comes next are instructions of
+// all its lanes. (The clock and the flag of another role can give its lanes different answers.)
+GNS_DEV bool fp4_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xFFFFFFFFu, fp4_wait(bar, parity, abort_flag, status));
+}
+
+// A last wait for what this CTA has under way, after a wait has run out: until the time `until` on the global timer.
+GNS_DEV bool fp4_settle(uint64_t* bar, uint32_t parity, uint64_t until) {
+  const uint32_t a = smem_u32(bar);
+  while (!mbar_try_wait(a, parity))
+    if (global_timer_ns() > until) return false;
+  return true;
+}
+
+// The operand ring as settle_ring() sees it, in the group's leader: bytes: what one CTA loads of a slice.
+struct Fp4Ring {
+  uint64_t* full;
+  uint32_t bytes;
+  uint64_t until;
+  GNS_DEV void forgo(uint32_t s) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[s])), "r"(bytes) : "memory");
+  }
+  GNS_DEV void announce(uint32_t s) { mbar_arrive_expect_tx(&full[s], bytes); }
+  GNS_DEV bool wait(uint32_t s, uint32_t parity) { return fp4_settle(&full[s], parity, until); }
+};
+
+// A word of shared memory in CTA `rank` of the cluster.
+GNS_DEV void store_cluster(void* at, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(at), rank)), "r"(v) : "memory");
 }
 
 // One lane of a converged warp, the same one each time.

@@ -219,7 +219,13 @@ GNS_DEV bool epilogue_tile(const GemmParams& P, const Tile& t, uint32_t acc, int
       if (lane == 0) bulk_wait_read<1>();
       __syncwarp();
     } else {
-      if (!fp4_wait(&cbar[chunk & 1], (chunk >> 1) & 1u, abort_flag, P.status)) return bad;
+      if (!fp4_warp_wait(&cbar[chunk & 1], (chunk >> 1) & 1u, abort_flag, P.status)) {
+        // nothing is left under way: neither this load nor the next chunk's values
+        if (!fp4_settle(&cbar[chunk & 1], (chunk >> 1) & 1u, global_timer_ns() + GNS_WAIT_TIMEOUT_NS)) set_status(P.status, GNS_DEVST_TIMEOUT);
+        __syncwarp();
+        tmem_ld_wait();
+        return bad;
+      }
       const float2 b2 = make_float2(P.beta, P.beta);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
@@ -297,8 +303,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* cbar = tempty + 2;  // two a warp of the epilogue
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cbar + 8);
+  uint64_t* mma_done = cbar + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* peer_abort = abort_flag + 1;
+  uint32_t* issued = tmem_slot + 3;  // slices that each CTA of the group has begun to load (the leader's copy)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
@@ -314,7 +323,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
       mbar_init(&tempty[a], CG * 4);
     }
     for (int i = 0; i < 8; ++i) mbar_init(&cbar[i], 1);
+    mbar_init(mma_done, 1);
     *abort_flag = 0;
+    *peer_abort = 0;
     mbar_fence_init();
     tma_prefetch_desc(&P.a);
     tma_prefetch_desc(&P.b);
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
       const uint32_t full0 = CG == 2 ? mapa_shared(smem_u32(&full[0]), 0) : smem_u32(&full[0]);
       const uint32_t base = smem_u32(smem);
       int s = 0;
-      uint32_t ph = 0;
+      uint32_t ph = 0, begun = 0;
       bool ok = true;
       for (long long tile = group; ok && tile < P.total; tile += ngroups) {
         const Tile t = tile_of(P, tile);
@@ -360,12 +371,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
           fp4_tma_load_3d<CG>(sa + L::A_BYTES, &P.b, fb, kb * ROW_BYTES, n0 + (int)rank * L::NB, t.b);
           fp4_tma_load_4d<CG>(sf, &P.sfa, fb, 0, kb * L::KT, m0 / 128, t.b);
           fp4_tma_load_4d<CG>(sf + L::SFA_BYTES, &P.sfb, fb, 0, kb * L::KT, n0 / 128, t.b);
+          ++begun;
           if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
+      if constexpr (CG == 2)
+        store_cluster(&issued[rank], 0, begun);
+      else
+        issued[0] = begun;
     }
   } else if (warp == 1) {
     if (rank == 0) {
@@ -384,16 +400,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
       for (long long tile = group; ok && tile < P.total; tile += ngroups, ++local) {
         const int acc = local % L::NACC;
         const uint32_t aph = (local / L::NACC) & 1;
-        if (!fp4_wait(&tempty[acc], aph ^ 1u, abort_flag, P.status)) break;
+        if (!(ok = fp4_warp_wait(&tempty[acc], aph ^ 1u, abort_flag, P.status))) break;
         tc_fence_after();
         const uint32_t d = tm + acc * BN;
         // B's first row in its first scale tile: 32 rows to a column
         const uint32_t sfb_0 = sfb_t + (BN % 128 ? (tile_of(P, tile).J * BN % 128) / 32 : 0);
         for (int kb = 0; kb < P.kblocks; ++kb) {
-          if (!fp4_wait(&full[s], ph, abort_flag, P.status)) {
-            ok = false;
-            break;
-          }
+          if (!(ok = fp4_warp_wait(&full[s], ph, abort_flag, P.status))) break;
           tc_fence_after();
           const uint32_t sa = base + s * (L::A_BYTES + L::B_BYTES);
           const uint32_t sf = base + L::OFF_SF + s * (L::SFA_BYTES + L::SFB_BYTES);
@@ -447,9 +460,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
       const int acc = local % L::NACC;
       const uint32_t aph = (local / L::NACC) & 1;
       const Factor f = factor_of(P, t.b);
-      if (!fp4_wait(&tfull[acc], aph, abort_flag, P.status)) break;
+      if (!fp4_warp_wait(&tfull[acc], aph, abort_flag, P.status)) break;
       tc_fence_after();
-      __syncwarp();
       const int row0 = t.I * TM * CG + (int)rank * TM + 32 * q;
       const uint32_t at = tmem + acc * BN + ((uint32_t)(32 * q) << 16);
       const bool mirror = P.sym && t.I != t.J;
@@ -468,7 +480,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
         else
           mbar_arrive(&tempty[acc]);
       }
-      if (*abort_flag) break;
+      if (__any_sync(0xFFFFFFFFu, *abort_flag)) break;
     }
     if (bad) set_status(P.status, GNS_DEVST_NONFINITE);
     if (lane == 0) bulk_wait_all();
@@ -477,7 +489,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync_all();
+  if constexpr (CG == 2) {
+    if (threadIdx.x == 0 && *abort_flag) store_cluster(const_cast<int*>(peer_abort), rank ^ 1u, 1u);
+    __syncwarp();
+    cluster_sync_all();
+  }
+  if (*abort_flag || *peer_abort) {  // a wait ran out; the same answer in every thread of the group, whose roles have all ended
+    const uint64_t until = global_timer_ns() + GNS_WAIT_TIMEOUT_NS;
+    bool ended = true;
+    if (rank == 0 && threadIdx.x == 0) {  // the operands' loads
+      Fp4Ring ring{full, (uint32_t)L::STAGE_BYTES, until};
+      ended = settle_ring(ring, issued[0], issued[CG - 1], (uint32_t)STAGES);
+    }
+    if (warp == 1 && elect_one()) {  // the MMAs, all issued by the leader's lane that is elected here
+      if constexpr (CG == 2) {
+        if (rank == 0) umma2_commit_multicast(mma_done, 0x3);
+      } else {
+        umma_commit(mma_done);
+      }
+      ended = fp4_settle(mma_done, 0u, until);
+    }
+    if (!ended) set_status(P.status, GNS_DEVST_TIMEOUT);
+    __syncwarp();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync_all();  // neither CTA leaves before the other's loads have landed
+  }
   if (warp == 1) {
     tc_fence_after();
     if constexpr (CG == 2)
