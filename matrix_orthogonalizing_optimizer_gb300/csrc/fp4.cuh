@@ -93,7 +93,10 @@ GNS_DEV bool fp4_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, 
 // The same for a whole converged warp, which goes on or gives up as one: what comes next are instructions of
 // all its lanes. (The clock and the flag of another role can give its lanes different answers.)
 GNS_DEV bool fp4_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  return __all_sync(0xFFFFFFFFu, fp4_wait(bar, parity, abort_flag, status));
+  const uint32_t a = smem_u32(bar);
+  for (int i = 0; i < 64; ++i)
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(a, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status));
 }
 
 // A last wait for what this CTA has under way, after a wait has run out: until the time `until` on the global timer.
