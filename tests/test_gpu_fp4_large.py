@@ -1,5 +1,5 @@
 """Matrices in 4 bits at the sizes where the large paths run: rings of operands that wrap, groups of CTAs with several tiles,
-quantisation in several launches, and what lies around and between the outputs."""
+the largest magnitudes of large matrices, and what lies around and between the outputs."""
 import functools
 
 import numpy as np
@@ -40,8 +40,8 @@ def test_gram_of_many_slices(fmt, shape):
         assert torch.equal(d, d.mT)
 
 
-def test_quantisation_in_several_launches():
-    """11 matrices of 5.7 MB: the largest magnitudes of eight are found in one launch, those of the last three in another."""
+def test_largest_magnitudes_of_many_large_matrices():
+    """11 matrices of 99 tiles each: one launch finds all their largest magnitudes, the next one takes each matrix's own."""
     x = matrices(95, (11, 1100, 1300), "f32") * (10.0 ** torch.arange(-5, 6))[:, None, None].float()
     d = padded(x)
     q, qt = gns.quantize_fp4(d, axes="both")
