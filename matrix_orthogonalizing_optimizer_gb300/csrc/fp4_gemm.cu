@@ -396,8 +396,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp4_gemm_kernel(const __grid_c
   } else if (warp == 1) {
     if (rank == 0) {
       // The whole warp walks the slices, and one elected lane issues: the operands of copies and MMAs
-      // then are in uniform registers. From a lane of its own, in divergent code, each of the 12 to 16
-      // instructions of a slice took 55 to 75 cycles to issue, more than the tensor cores need.
+      // then are in uniform registers. When a lane of its own issued them, in divergent code, issue and not the
+      // tensor cores bounded the kernel (with that, and a slower epilogue, 16384 x 11008 x 4096 in 128 x 128 tiles
+      // took 653 us, against 382).
       const uint32_t base = __shfl_sync(0xFFFFFFFFu, smem_u32(smem), 0);
       const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
       const uint32_t sfa_t = tm + L::NACC * BN;
@@ -660,11 +661,12 @@ int launch(const Fp4Product& p, int32_t* status, cudaStream_t stream, std::strin
 // 128 x 128 tiles of single CTAs, or tiles of CTA pairs: 256 x 192 (two accumulators in tensor memory) for
 // A B^T, 256 x 256 (one accumulator; a symmetric product's tiles are square) for X X^T. A pair tile
 // reads less per product from L2, which bounds the small one, and fills the SMs less evenly. What counts is
-// the number of waves over the SMs, weighted by what one costs (measured, K from 4096 to 8192: a wave of
-// 256 x 192 tiles takes about 1.1, of 256 x 256 tiles 1.6 to 1.9 times one of 128 x 128). bf16 results,
-// 128 x 128 against the pair's, us: 16384 x 11008 x 4096 378 / 273, 4096 x 11008 x 4096 103 / 76, 512 x 4096 x
-// 4096 9.4 / 11.0, 16 of 1024 x 1024 x 2048 25.5 / 28.8; X X^T of 16 of 2048 x 8192 151 / 127, of 24 of
-// 1024 x 4096 37.7 / 47.
+// the number of waves over the SMs, weighted by what one costs (a wave of 256 x 192 tiles about 1.1 to 1.2, of
+// 256 x 256 tiles 1.6 to 1.9 times one of 128 x 128, for K of 4096 and more). NVFP4 with bf16 results in a captured graph,
+// us, 128 x 128 against the pair's: 16384 x 11008 x 4096 382 / 277, 4096 x 11008 x 4096 103 / 79, 512 x 4096 x
+// 4096 10.6 / 12.3, 16 of 1024 x 1024 x 2048 26.5 / 30.5; X X^T of 16 of 2048 x 8192 153 / 132, of 24 of
+// 1024 x 4096 39 / 48. MXFP4 is within 3 % of that. Short K and fp32 results weigh the epilogue, which the rule does not:
+// 2048 x 4096 x 1024 takes pairs with 14.6 / 16.8, 4096 x 4096 of X X^T in fp32 with 31.5 / 33.5.
 template <int FMT>
 int launch_format(const Fp4Product& p, int32_t* status, cudaStream_t stream, std::string* err) {
   const long long sms = device_sm_count(), M = p.a.rows, N = p.b.rows;
