@@ -231,7 +231,8 @@ GNS_DEV bool epilogue_tile(const GemmParams& P, const Tile& t, uint32_t acc, int
     } else {
       if (!fp4_warp_wait(&cbar[chunk & 1], (chunk >> 1) & 1u, abort_flag, P.status)) {
         // nothing is left under way: neither this load nor the next chunk's values
-        if (!fp4_settle(&cbar[chunk & 1], (chunk >> 1) & 1u, global_timer_ns() + GNS_WAIT_TIMEOUT_NS)) set_status(P.status, GNS_DEVST_TIMEOUT);
+        if (!fp4_settle(&cbar[chunk & 1], (chunk >> 1) & 1u, global_timer_ns() + GNS_WAIT_TIMEOUT_NS))
+          set_status(P.status, GNS_DEVST_TIMEOUT);
         __syncwarp();
         tmem_ld_wait();
         return bad;
